@@ -13,7 +13,8 @@
  *                       ("AttnV41", decode_fixed_topk / decode_prep)
  *
  * Conventions shared by every entry point
- *   - Element type: every q / k / v / out buffer holds bfloat16 values (2 bytes each); the
+ *   - Element type: every q / k / v / out buffer holds bfloat16 values (2 bytes each; the quantised
+ *     pool holds codes, see there); the
  *     arithmetic is fp32 (scores, online softmax, accumulation), the output is rounded to bf16
  *     round-to-nearest-even.
  *   - Pointers: q, k, v, pools, out, block_table, kv_lens, sel and the workspace are DEVICE
@@ -68,7 +69,8 @@ typedef enum {
     DA_ERR_CUDA = 4                /* a CUDA runtime call or kernel launch failed */
 } da_status;
 
-typedef enum { DA_VARIANT_DENSE = 0, DA_VARIANT_PAGED = 1, DA_VARIANT_SPARSE = 2 } da_variant;
+typedef enum { DA_VARIANT_DENSE = 0, DA_VARIANT_PAGED = 1, DA_VARIANT_SPARSE = 2,
+               DA_VARIANT_PAGED_QUANT = 3 } da_variant;
 
 /* DECODE_ATTN_ABI_VERSION of the built library. */
 int decode_attn_abi_version(void);
@@ -192,6 +194,72 @@ da_status decode_attn_append_paged(const void *k_new, const void *v_new, void *k
 da_status decode_attn_append_ring(const void *k_new, const void *v_new, void *k_pool,
                                   void *v_pool, const int64_t *positions, int B, int Hkv, int D,
                                   int64_t pool_rows, int window, void *stream);
+
+/*
+ * The quantised paged cache: keys and values in codes of 4 or 8 bits, with one writer, one reader
+ * and one attention call.  No counterpart in the pages: the format and its calls are additions of
+ * this library, beside the bf16 paged cache above.
+ *
+ * pool: uint8 [num_pages, Hkv, page_bytes], page_bytes = decode_attn_quant_page_bytes().  Each row of
+ * D elements is cut into groups of `group` elements; a group of K (and one of V) keeps a scale and a
+ * minimum in bf16 and one code per element that stands for min + scale * code:
+ *   min    the group's smallest element
+ *   scale  (largest - smallest) / (2^bits - 1), rounded up to bf16 (0 below 2^-126)
+ *   code   (x - min) / scale to the nearest integer, ties to even (0 where scale is 0)
+ * so an element is off by at most scale / 2 before bf16 rounding.  A group that holds a NaN or an
+ * infinity, or whose range passes the largest fp32, reads as NaN throughout.
+ * A page of one KV head holds the K codes of its rows, their V codes, then per row D / group
+ * quadruples (k_scale, k_min, v_scale, v_min) of bf16; a row is 2 D bits / 8 + 8 D / group bytes (D =
+ * 128 in 4 bits: 136 with one group against 512 in bf16).  Codes are stored in the order the
+ * attention kernel reads them: element 16 s + 4 t + i of a K row is code (t D / 16 + s) 4 + i of its
+ * stored row, element 16 m + 2 g + i of a V row is code (g D / 16 + m) 2 + i; two 4-bit codes share a
+ * byte, the first one in its low half.
+ *   bits in {4, 8}; group in {32, 64, 128}, at most D; D in {64, 128}; page_size a power of two in
+ *   [8, 256]; Hkv < 4096; pool 16-byte aligned.  Anything else is DA_ERR_UNSUPPORTED.
+ */
+
+/* Bytes of one page of one KV head; 0 for a format that the calls would refuse.  Host only. */
+size_t decode_attn_quant_page_bytes(int D, int page_size, int bits, int group);
+
+/*
+ * Quantises new rows into the cache as it is written: decode_attn_append_paged for this format.
+ * Row t of k_new / v_new (bf16 [T, Hkv, D], rows k_row_stride / v_row_stride elements apart, heads
+ * contiguous, so the K and V parts of one projection can be given as they lie) goes to slot
+ * slot_mapping[t] (i64, device memory) of every KV head; a slot outside [0, num_pages * page_size)
+ * writes nothing, and no other byte of the pool changes.  Give a slot at most once per call: rows
+ * that name the same slot leave that slot's contents undefined (and only those).
+ *   k_new, v_new 16-byte aligned; strides at least Hkv * D and multiples of 8.
+ */
+da_status decode_attn_append_paged_quant(const void *k_new, const void *v_new, int64_t k_row_stride,
+                                         int64_t v_row_stride, void *pool,
+                                         const int64_t *slot_mapping, int64_t T, int Hkv, int D,
+                                         int page_size, int64_t num_pages, int bits, int group,
+                                         void *stream);
+
+/*
+ * Reads rows back: row t of k_out / v_out (bf16 [T, Hkv, D]) becomes what slot slot_mapping[t] stands
+ * for, min + scale * code in fp32 rounded to bf16 (for a chunk of a prompt that attends to what is
+ * already cached, or a prefix that leaves the cache).  A slot outside the pool gives zero rows; a
+ * slot may be named any number of times.  k_out, v_out 16-byte aligned.
+ */
+da_status decode_attn_read_paged_quant(const void *pool, const int64_t *slot_mapping, void *k_out,
+                                       void *v_out, int64_t T, int Hkv, int D, int page_size,
+                                       int64_t num_pages, int bits, int group, void *stream);
+
+/*
+ * Paged decode attention over the quantised cache: decode_attn_paged_mq for this format.  q, out
+ * bf16 [B, Hq, Sq, D] (Sq = 1 for a plain decode step), block table, lengths, clamping, bad page ids,
+ * empty rows, causal masking and limits as there; the codes are multiplied as they are, exactly, and
+ * scales and minima are applied in fp32.  Requires (Hq / Hkv) * Sq <= 64 and max_pages_per_seq *
+ * page_size < 2^31 - 256.  Workspace: decode_attn_workspace_size(DA_VARIANT_PAGED_QUANT, B, Hq * Sq,
+ * Hkv, D, 0).  Scales are expected non-negative, as the writer stores them.
+ */
+da_status decode_attn_paged_quant(const void *q, const void *pool, void *out,
+                                  const int32_t *block_table, int max_pages_per_seq, int page_size,
+                                  int64_t num_pages, const uint32_t *kv_lens, int kv_len_stride,
+                                  int B, int Hq, int Hkv, int D, int Sq, int causal, int bits,
+                                  int group, float softmax_scale, void *workspace,
+                                  size_t workspace_bytes, void *stream);
 
 /*
  * The options of a decode-attention region, as "DecodeFlashSpec" (docs.rs

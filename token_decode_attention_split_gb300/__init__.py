@@ -13,7 +13,9 @@ _BINDING_NAMES = (
     "decode_attn_paged_mq", "decode_attn_check_wait_timeout", "decode_attn_spec_check",
     "decode_attn_dense_spec", "decode_attn_dense_noalloc", "decode_attn_status_string",
     "decode_attn_abi_version", "DecodeAttnSpec",
-    "DA_VARIANT_DENSE", "DA_VARIANT_PAGED", "DA_VARIANT_SPARSE",
+    "decode_attn_quant_page_bytes", "new_quant_pool", "decode_attn_append_paged_quant",
+    "decode_attn_read_paged_quant", "decode_attn_paged_quant",
+    "DA_VARIANT_DENSE", "DA_VARIANT_PAGED", "DA_VARIANT_SPARSE", "DA_VARIANT_PAGED_QUANT",
 )
 
 

@@ -14,7 +14,7 @@ import torch
 
 from . import build as _build
 
-DA_VARIANT_DENSE, DA_VARIANT_PAGED, DA_VARIANT_SPARSE = 0, 1, 2
+DA_VARIANT_DENSE, DA_VARIANT_PAGED, DA_VARIANT_SPARSE, DA_VARIANT_PAGED_QUANT = 0, 1, 2, 3
 _lock = threading.Lock()
 _lib = None
 
@@ -88,6 +88,16 @@ def load_library() -> ctypes.CDLL:
                                                i, i64, i64, vp, sz, vp]
         lib.decode_attn_dense_noalloc.restype = i
         lib.decode_attn_dense_noalloc.argtypes = [vp, vp, vp, vp, i, i, i, i, i64, i64, f, vp]
+        lib.decode_attn_quant_page_bytes.restype = sz
+        lib.decode_attn_quant_page_bytes.argtypes = [i, i, i, i]
+        lib.decode_attn_append_paged_quant.restype = i
+        lib.decode_attn_append_paged_quant.argtypes = [vp, vp, i64, i64, vp, vp, i64, i, i, i, i64,
+                                                       i, i, vp]
+        lib.decode_attn_read_paged_quant.restype = i
+        lib.decode_attn_read_paged_quant.argtypes = [vp, vp, vp, vp, i64, i, i, i, i64, i, i, vp]
+        lib.decode_attn_paged_quant.restype = i
+        lib.decode_attn_paged_quant.argtypes = [vp, vp, vp, vp, i, i, i64, vp, i, i, i, i, i, i, i,
+                                                i, i, f, vp, sz, vp]
         _lib = lib
         return lib
 
@@ -276,6 +286,126 @@ def decode_attn_append_ring(k_new, v_new, k_pool, v_pool, positions, window: int
     _check(load_library().decode_attn_append_ring(
         _ptr(k_new), _ptr(v_new), _ptr(k_pool), _ptr(v_pool), _ptr(positions), B, Hkv, D,
         k_pool.shape[2], int(window), _stream(stream, k_new.device)), "decode_attn_append_ring")
+
+
+def decode_attn_quant_page_bytes(D: int, page_size: int, bits: int, group: int) -> int:
+    """Bytes of one page of one KV head of the quantised cache (0: a format the calls refuse)."""
+    return int(load_library().decode_attn_quant_page_bytes(int(D), int(page_size), int(bits),
+                                                           int(group)))
+
+
+def new_quant_pool(num_pages: int, Hkv: int, D: int, page_size: int, bits: int, group: int,
+                   device) -> torch.Tensor:
+    """A zero-filled pool of the quantised cache, uint8 [num_pages, Hkv, page_bytes]."""
+    nbytes = decode_attn_quant_page_bytes(D, page_size, bits, group)
+    if nbytes == 0:
+        raise ValueError(f"no quantised cache for D={D}, page_size={page_size}, bits={bits}, "
+                         f"group={group}")
+    return torch.zeros(num_pages, Hkv, nbytes, dtype=torch.uint8, device=device)
+
+
+def _want(t, name: str, dtype, dim: int, device):
+    """A contiguous tensor of that type and rank on that device, or a ValueError."""
+    if t.dtype != dtype or t.dim() != dim or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dim}-d {dtype} tensor on {device}")
+
+
+def _quant_page_size(pool, D: int, bits: int, group: int) -> int:
+    """Page size of a quantised pool [num_pages, Hkv, page_bytes]."""
+    if pool.dtype != torch.uint8 or pool.dim() != 3 or not pool.is_contiguous() or not pool.is_cuda:
+        raise ValueError("pool must be a contiguous uint8 CUDA tensor [num_pages, Hkv, page_bytes]")
+    if D <= 0 or bits <= 0 or group <= 0 or D % group:
+        raise ValueError(f"no rows of {D} elements in groups of {group} with {bits} bits")
+    row = 2 * D * bits // 8 + D // group * 8
+    if pool.shape[2] == 0 or pool.shape[2] % row:
+        raise ValueError(f"pages of {pool.shape[2]} bytes hold no whole rows of {row} bytes")
+    return pool.shape[2] // row
+
+
+def _quant_rows(t, name: str, pool, T: int, Hkv: int, D: int, contiguous: bool) -> int:
+    """Checks bf16 rows [T, Hkv, D] beside a pool; their row stride in elements."""
+    if t.dtype != torch.bfloat16 or tuple(t.shape) != (T, Hkv, D) or t.device != pool.device:
+        raise ValueError(f"{name} must be bf16 [{T}, {Hkv}, {D}] on {pool.device}")
+    packed = (D == 1 or t.stride(2) == 1) and (Hkv == 1 or t.stride(1) == D)
+    if t.numel() and (not packed or (contiguous and not t.is_contiguous())):
+        raise ValueError(f"{name}: the heads of a row must be contiguous"
+                         + (", and the rows too" if contiguous else ""))
+    return t.stride(0) if T > 1 else Hkv * D
+
+
+def _on(device):
+    """The library launches on the current device: make it the tensors' own."""
+    return torch.cuda.device(device)
+
+
+def decode_attn_append_paged_quant(k_new, v_new, pool, slot_mapping, bits: int, group: int,
+                                   stream=None):
+    """Quantises k_new, v_new (bf16 [T,Hkv,D], rows any stride apart) into the slots slot_mapping
+    (int64 [T]) of a quantised pool [num_pages,Hkv,page_bytes] (new_quant_pool)."""
+    T, Hkv, D = k_new.shape
+    P = _quant_page_size(pool, D, bits, group)
+    ks = _quant_rows(k_new, "k_new", pool, T, pool.shape[1], D, False)
+    vs = _quant_rows(v_new, "v_new", pool, T, pool.shape[1], D, False)
+    _want(slot_mapping, "slot_mapping", torch.int64, 1, pool.device)
+    if slot_mapping.shape[0] != T:
+        raise ValueError("slot_mapping must name one slot per row")
+    if T == 0:
+        return
+    with _on(pool.device):
+        _check(load_library().decode_attn_append_paged_quant(
+            _ptr(k_new), _ptr(v_new), ks, vs, _ptr(pool), _ptr(slot_mapping), T, Hkv, D, P,
+            pool.shape[0], int(bits), int(group), _stream(stream, pool.device)),
+            "decode_attn_append_paged_quant")
+
+
+def decode_attn_read_paged_quant(pool, slot_mapping, k_out, v_out, bits: int, group: int,
+                                 stream=None):
+    """Reads the slots slot_mapping (int64 [T]) of a quantised pool into k_out, v_out (bf16
+    [T,Hkv,D], contiguous); a slot outside the pool gives zero rows."""
+    T, Hkv, D = k_out.shape
+    P = _quant_page_size(pool, D, bits, group)
+    _quant_rows(k_out, "k_out", pool, T, pool.shape[1], D, True)
+    _quant_rows(v_out, "v_out", pool, T, pool.shape[1], D, True)
+    _want(slot_mapping, "slot_mapping", torch.int64, 1, pool.device)
+    if slot_mapping.shape[0] != T:
+        raise ValueError("slot_mapping must name one slot per row")
+    if T == 0:
+        return k_out, v_out
+    with _on(pool.device):
+        _check(load_library().decode_attn_read_paged_quant(
+            _ptr(pool), _ptr(slot_mapping), _ptr(k_out), _ptr(v_out), T, Hkv, D, P, pool.shape[0],
+            int(bits), int(group), _stream(stream, pool.device)), "decode_attn_read_paged_quant")
+    return k_out, v_out
+
+
+def decode_attn_paged_quant(q, pool, out, block_table, kv_lens, kv_len_stride: int, bits: int,
+                            group: int, causal: bool, softmax_scale: float, workspace, stream=None):
+    """q, out [B,Hq,Sq,D] bf16; a quantised pool [num_pages,Hkv,page_bytes]; block table and
+    lengths as for decode_attn_paged.  Workspace: decode_attn_workspace_size(
+    DA_VARIANT_PAGED_QUANT, B, Hq * Sq, Hkv, D)."""
+    B, Hq, Sq, D = q.shape
+    P = _quant_page_size(pool, D, bits, group)
+    dev = pool.device
+    _want(q, "q", torch.bfloat16, 4, dev)
+    _want(out, "out", torch.bfloat16, 4, dev)
+    _want(block_table, "block_table", torch.int32, 2, dev)
+    if out.shape != q.shape or block_table.shape[0] != B:
+        raise ValueError("out must have q's shape and block_table a row per sequence")
+    if not kv_lens.is_contiguous() or kv_lens.device != dev or kv_lens.element_size() != 4 or \
+            kv_lens.numel() < (B - 1) * kv_len_stride + 1:
+        raise ValueError("kv_lens must hold a 32-bit length per sequence on the pool's device")
+    if workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous buffer on the pool's device")
+    if q.numel() == 0:
+        return out
+    with _on(dev):
+        _check(load_library().decode_attn_paged_quant(
+            _ptr(q), _ptr(pool), _ptr(out), _ptr(block_table), block_table.shape[1], P,
+            pool.shape[0], _ptr(kv_lens), int(kv_len_stride), B, Hq, pool.shape[1], D, Sq,
+            int(bool(causal)), int(bits), int(group), float(softmax_scale), _ptr(workspace),
+            workspace.numel() * workspace.element_size(), _stream(stream, dev)),
+            "decode_attn_paged_quant")
+    return out
 
 
 def run_case(case, out=None, workspace=None, stream=None):

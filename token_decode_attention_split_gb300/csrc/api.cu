@@ -14,6 +14,7 @@
 
 #include "decode_attn.h"
 #include "launch.h"
+#include "quant_attn.cuh"
 
 namespace da {
 
@@ -188,6 +189,16 @@ int paged_kv_heads(int Hkv, int G, int page_size) {
 // Dense units of at most this many 64-row tiles are not split across CTAs.
 constexpr long long kShortUnitTiles = 8;
 
+// Quantised paged units: warps that split a KV head's `cols` query columns (log2), and the KV heads
+// per unit for that many -- the most (a power of two dividing Hkv) that still leave each head a warp
+// of every eight.
+int quant_slices_shift(int cols) { return cols <= 16 ? 0 : cols <= 32 ? 1 : 2; }
+int quant_kv_heads(int Hkv, int cols) {
+    int kh = 1;
+    while (Hkv % (2 * kh) == 0 && (2 * kh << quant_slices_shift(cols)) <= 8) kh *= 2;
+    return kh;
+}
+
 // CTAs for a persistent dense/paged launch on `dev`.
 int persistent_ctas(int dev) {
     const int sms = sm_count(dev);
@@ -219,7 +230,8 @@ unsigned long long current_context_id() {
     return get_id(ctx, &id) == CUDA_SUCCESS ? id : 0;
 }
 
-cudaError_t launch_kernel(const void* kernel, int smem, const Launch& L) {
+cudaError_t launch_configured(const void* kernel, int smem, int grid, int threads,
+                              cudaStream_t stream, void** args) {
     const int dev = current_device();
     if (dev < 0) return cudaErrorInvalidDevice;
     const unsigned long long ctx = current_context_id();
@@ -236,21 +248,25 @@ cudaError_t launch_kernel(const void* kernel, int smem, const Launch& L) {
             g_configured.insert({kernel, ctx});
         }
     }
-    void* args[] = {const_cast<CUtensorMap*>(&L.tm_k), const_cast<CUtensorMap*>(&L.tm_v),
-                    const_cast<Params*>(&L.p)};
     // Programmatic stream serialization: the kernel may be scheduled while the previous kernel
     // in the stream drains; it waits for that kernel's completion before touching memory.
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(L.grid);
-    cfg.blockDim = dim3(L.threads);
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = static_cast<size_t>(smem);
-    cfg.stream = L.stream;
+    cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelExC(&cfg, kernel, args);
+}
+
+cudaError_t launch_kernel(const void* kernel, int smem, const Launch& L) {
+    void* args[] = {const_cast<CUtensorMap*>(&L.tm_k), const_cast<CUtensorMap*>(&L.tm_v),
+                    const_cast<Params*>(&L.p)};
+    return launch_configured(kernel, smem, L.grid, L.threads, L.stream, args);
 }
 
 }  // namespace da
@@ -278,11 +294,16 @@ size_t decode_attn_workspace_size(int variant, int B, int Hq, int Hkv, int D, in
     if (padded_group(G) == 0) return 0;
     const long long units = static_cast<long long>(B) * Hkv;
     long long segments = 0;
-    if (variant == DA_VARIANT_DENSE || variant == DA_VARIANT_PAGED) {
+    if (variant == DA_VARIANT_DENSE || variant == DA_VARIANT_PAGED ||
+        variant == DA_VARIANT_PAGED_QUANT) {
         const int dev = current_device();
         if (dev < 0) return 0;
         const int sms = sm_count(dev);
         if (sms <= 0) return 0;
+        if (variant == DA_VARIANT_PAGED_QUANT) {
+            const int kh = quant_kv_heads(Hkv, G);
+            return ws_layout(units / kh, units / kh + sms, kh * G, D).total;
+        }
         if (variant == DA_VARIANT_PAGED) {
             // the page size is not an argument here: size for every unit width a call may use
             size_t most = 0;
@@ -614,3 +635,66 @@ da_status decode_attn_sparse(const void* q, const void* k_pool, const void* v_po
 }
 
 }  // extern "C"
+
+extern "C" da_status decode_attn_paged_quant(
+    const void* q, const void* pool, void* out, const int32_t* block_table, int max_pages_per_seq,
+    int page_size, int64_t num_pages, const uint32_t* kv_lens, int kv_len_stride, int B, int Hq,
+    int Hkv, int D, int Sq, int causal, int bits, int group, float softmax_scale, void* workspace,
+    size_t workspace_bytes, void* stream) {
+    da_status st = check_common(q, out, B, Hq, Hkv, D, softmax_scale, workspace);
+    if (st != DA_OK) return st;
+    if (Sq < 1) return DA_ERR_INVALID_ARGUMENT;
+    if (Sq > 64 || padded_group((Hq / Hkv) * Sq) == 0) return DA_ERR_UNSUPPORTED;
+    if (!pool || !aligned(pool, 16)) return DA_ERR_INVALID_ARGUMENT;
+    if (!block_table || !kv_lens || !aligned(block_table, 4) || !aligned(kv_lens, 4))
+        return DA_ERR_INVALID_ARGUMENT;
+    if (max_pages_per_seq < 1 || page_size < 1 || num_pages < 1) return DA_ERR_INVALID_ARGUMENT;
+    if (kv_len_stride != 1 && kv_len_stride != 3) return DA_ERR_INVALID_ARGUMENT;
+    if (!quant_format_ok(D, page_size, bits, group)) return DA_ERR_UNSUPPORTED;
+    if (num_pages >= (1ll << 31) || Hkv >= (1 << 12) || B > kMaxPagedBatch) return DA_ERR_UNSUPPORTED;
+    const long long cap = static_cast<long long>(max_pages_per_seq) * page_size;
+    if (cap >= (1ll << 31) - 256) return DA_ERR_UNSUPPORTED;
+    const long long units = static_cast<long long>(B) * Hkv;
+    if (units * ((cap + 15) / 16) >= (1ll << 31)) return DA_ERR_UNSUPPORTED;
+    if (B == 0) return DA_OK;
+    const int dev = current_device();
+    if (dev < 0) return DA_ERR_CUDA;
+    const int sms = sm_count(dev);
+    if (sms <= 0) return DA_ERR_CUDA;
+    QuantParams p{};
+    p.cols = (Hq / Hkv) * Sq;
+    p.kh = quant_kv_heads(Hkv, p.cols);
+    const long long qunits = units / p.kh;
+    const WsLayout w = ws_layout(qunits, qunits + sms, p.kh * p.cols, D);
+    if (workspace_bytes < w.total) return DA_ERR_WORKSPACE_TOO_SMALL;
+    p.q = static_cast<const __nv_bfloat16*>(q);
+    p.out = static_cast<__nv_bfloat16*>(out);
+    p.pool = static_cast<const unsigned char*>(pool);
+    p.block_table = block_table;
+    p.kv_lens = kv_lens;
+    p.kv_stride = kv_len_stride;
+    p.max_pages = max_pages_per_seq;
+    p.page_size = page_size;
+    p.num_pages = static_cast<int>(num_pages);
+    p.B = B;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.sq = Sq;
+    p.causal = causal ? 1 : 0;
+    p.slices_shift = quant_slices_shift(p.cols);
+    p.scale_log2 = softmax_scale * 1.4426950408889634f;
+    unsigned char* base = static_cast<unsigned char*>(workspace);
+    p.counters = reinterpret_cast<unsigned*>(base + w.counters);
+    p.part_lse = reinterpret_cast<float*>(base + w.lse);
+    p.part_o = reinterpret_cast<float*>(base + w.o);
+    p.err = device_error_ptr(dev);
+    const int grid = persistent_ctas(dev), groups = D / group;
+    const bool narrow = p.cols <= 8;
+    const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    const cudaError_t e =
+        D == 64 ? (bits == 4 ? launch_quant<64, 4>(groups, narrow, p, grid, cs)
+                             : launch_quant<64, 8>(groups, narrow, p, grid, cs))
+                : (bits == 4 ? launch_quant<128, 4>(groups, narrow, p, grid, cs)
+                             : launch_quant<128, 8>(groups, narrow, p, grid, cs));
+    return e == cudaSuccess ? DA_OK : DA_ERR_CUDA;
+}

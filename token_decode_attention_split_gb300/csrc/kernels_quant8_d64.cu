@@ -1,0 +1,13 @@
+// quantised paged decode-attention kernel instantiations: head dim 64, 8-bit codes, every group size,
+// up to 8 and up to 16 query columns per warp.
+#include "quant_attn.cuh"
+
+namespace da {
+
+template <>
+cudaError_t launch_quant<64, 8>(int groups, bool narrow, const QuantParams& p, int grid,
+                                 cudaStream_t st) {
+    return launch_quant_any<64, 8>(groups, narrow, p, grid, st);
+}
+
+}  // namespace da

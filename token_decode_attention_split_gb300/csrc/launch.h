@@ -38,6 +38,8 @@ cudaError_t launch_wait_check(unsigned* err, uint64_t limit_ns, cudaStream_t str
 // Opts the kernel into `smem` bytes of dynamic shared memory on the current device (once per
 // kernel and CUDA context), then launches it with L.threads threads per block.
 cudaError_t launch_kernel(const void* kernel, int smem, const Launch& L);
-
+// The same for any kernel and arguments.
+cudaError_t launch_configured(const void* kernel, int smem, int grid, int threads,
+                              cudaStream_t stream, void** args);
 
 }  // namespace da
