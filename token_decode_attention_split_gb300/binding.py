@@ -304,77 +304,97 @@ def new_quant_pool(num_pages: int, Hkv: int, D: int, page_size: int, bits: int, 
     return torch.zeros(num_pages, Hkv, nbytes, dtype=torch.uint8, device=device)
 
 
-def _want(t, name: str, dtype, dim: int, device):
-    """A contiguous tensor of that type and rank on that device, or a ValueError."""
-    if t.dtype != dtype or t.dim() != dim or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dim}-d {dtype} tensor on {device}")
+def _refuse(what: str):
+    raise ValueError(what)
 
 
 def _quant_page_size(pool, D: int, bits: int, group: int) -> int:
     """Page size of a quantised pool [num_pages, Hkv, page_bytes]."""
     if pool.dtype != torch.uint8 or pool.dim() != 3 or not pool.is_contiguous() or not pool.is_cuda:
-        raise ValueError("pool must be a contiguous uint8 CUDA tensor [num_pages, Hkv, page_bytes]")
+        _refuse("pool must be a contiguous uint8 CUDA tensor [num_pages, Hkv, page_bytes]")
     if D <= 0 or bits <= 0 or group <= 0 or D % group:
-        raise ValueError(f"no rows of {D} elements in groups of {group} with {bits} bits")
+        _refuse(f"no rows of {D} elements in groups of {group} with {bits} bits")
     row = 2 * D * bits // 8 + D // group * 8
-    if pool.shape[2] == 0 or pool.shape[2] % row:
-        raise ValueError(f"pages of {pool.shape[2]} bytes hold no whole rows of {row} bytes")
-    return pool.shape[2] // row
+    nbytes = pool.shape[2]
+    if nbytes == 0 or nbytes % row:
+        _refuse(f"pages of {nbytes} bytes hold no whole rows of {row} bytes")
+    return nbytes // row
 
 
-def _quant_rows(t, name: str, pool, T: int, Hkv: int, D: int, contiguous: bool) -> int:
+def _quant_rows(t, name: str, pool, shape, contiguous: bool) -> int:
     """Checks bf16 rows [T, Hkv, D] beside a pool; their row stride in elements."""
-    if t.dtype != torch.bfloat16 or tuple(t.shape) != (T, Hkv, D) or t.device != pool.device:
-        raise ValueError(f"{name} must be bf16 [{T}, {Hkv}, {D}] on {pool.device}")
-    packed = (D == 1 or t.stride(2) == 1) and (Hkv == 1 or t.stride(1) == D)
-    if t.numel() and (not packed or (contiguous and not t.is_contiguous())):
-        raise ValueError(f"{name}: the heads of a row must be contiguous"
-                         + (", and the rows too" if contiguous else ""))
-    return t.stride(0) if T > 1 else Hkv * D
+    if t.dtype != torch.bfloat16 or t.shape != shape or t.get_device() != pool.get_device():
+        _refuse(f"{name} must be bf16 {list(shape)} on {pool.device}")
+    if t.is_contiguous():
+        return shape[1] * shape[2]
+    if contiguous or t.stride(2) != 1 or (shape[1] > 1 and t.stride(1) != shape[2]):
+        _refuse(f"{name}: the heads of a row must be contiguous" + (", and the rows too" if contiguous
+                                                                    else ""))
+    return t.stride(0) if shape[0] > 1 else shape[1] * shape[2]
 
 
-def _on(device):
-    """The library launches on the current device: make it the tensors' own."""
-    return torch.cuda.device(device)
+def _quant_slots(slot_mapping, T: int, pool):
+    if slot_mapping.dtype != torch.int64 or slot_mapping.shape != (T,) or \
+            not slot_mapping.is_contiguous() or slot_mapping.get_device() != pool.get_device():
+        _refuse(f"slot_mapping must be a contiguous int64 [{T}] on {pool.device}")
+
+
+def _call_on(index: int, name: str, stream, *args):
+    """Calls a library function (whose last argument is the stream) with CUDA device `index`
+    current: it launches on the current device."""
+    if torch.cuda.current_device() != index:
+        with torch.cuda.device(index):
+            return _call_on(index, name, stream, *args)
+    if stream is None:
+        raw = _current_raw_stream(index)
+    else:
+        raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    status = getattr(_lib or load_library(), name)(*args, raw)
+    if status:
+        _check(status, name)
+
+
+def _current_raw_stream(index: int) -> int:
+    """cudaStream_t of torch's current stream, without building a Stream object where torch can."""
+    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return get(index) if get is not None else torch.cuda.current_stream(index).cuda_stream
 
 
 def decode_attn_append_paged_quant(k_new, v_new, pool, slot_mapping, bits: int, group: int,
                                    stream=None):
     """Quantises k_new, v_new (bf16 [T,Hkv,D], rows any stride apart) into the slots slot_mapping
     (int64 [T]) of a quantised pool [num_pages,Hkv,page_bytes] (new_quant_pool)."""
-    T, Hkv, D = k_new.shape
+    shape = k_new.shape
+    T, Hkv, D = shape
     P = _quant_page_size(pool, D, bits, group)
-    ks = _quant_rows(k_new, "k_new", pool, T, pool.shape[1], D, False)
-    vs = _quant_rows(v_new, "v_new", pool, T, pool.shape[1], D, False)
-    _want(slot_mapping, "slot_mapping", torch.int64, 1, pool.device)
-    if slot_mapping.shape[0] != T:
-        raise ValueError("slot_mapping must name one slot per row")
+    if pool.shape[1] != Hkv:
+        _refuse(f"rows of {Hkv} KV heads beside a pool of {pool.shape[1]}")
+    ks = _quant_rows(k_new, "k_new", pool, shape, False)
+    vs = _quant_rows(v_new, "v_new", pool, shape, False)
+    _quant_slots(slot_mapping, T, pool)
     if T == 0:
         return
-    with _on(pool.device):
-        _check(load_library().decode_attn_append_paged_quant(
-            _ptr(k_new), _ptr(v_new), ks, vs, _ptr(pool), _ptr(slot_mapping), T, Hkv, D, P,
-            pool.shape[0], int(bits), int(group), _stream(stream, pool.device)),
-            "decode_attn_append_paged_quant")
+    _call_on(pool.get_device(), "decode_attn_append_paged_quant", stream, k_new.data_ptr(),
+             v_new.data_ptr(), ks, vs, pool.data_ptr(), slot_mapping.data_ptr(), T, Hkv, D, P,
+             pool.shape[0], bits, group)
 
 
 def decode_attn_read_paged_quant(pool, slot_mapping, k_out, v_out, bits: int, group: int,
                                  stream=None):
     """Reads the slots slot_mapping (int64 [T]) of a quantised pool into k_out, v_out (bf16
     [T,Hkv,D], contiguous); a slot outside the pool gives zero rows."""
-    T, Hkv, D = k_out.shape
+    shape = k_out.shape
+    T, Hkv, D = shape
     P = _quant_page_size(pool, D, bits, group)
-    _quant_rows(k_out, "k_out", pool, T, pool.shape[1], D, True)
-    _quant_rows(v_out, "v_out", pool, T, pool.shape[1], D, True)
-    _want(slot_mapping, "slot_mapping", torch.int64, 1, pool.device)
-    if slot_mapping.shape[0] != T:
-        raise ValueError("slot_mapping must name one slot per row")
-    if T == 0:
-        return k_out, v_out
-    with _on(pool.device):
-        _check(load_library().decode_attn_read_paged_quant(
-            _ptr(pool), _ptr(slot_mapping), _ptr(k_out), _ptr(v_out), T, Hkv, D, P, pool.shape[0],
-            int(bits), int(group), _stream(stream, pool.device)), "decode_attn_read_paged_quant")
+    if pool.shape[1] != Hkv:
+        _refuse(f"rows of {Hkv} KV heads beside a pool of {pool.shape[1]}")
+    _quant_rows(k_out, "k_out", pool, shape, True)
+    _quant_rows(v_out, "v_out", pool, shape, True)
+    _quant_slots(slot_mapping, T, pool)
+    if T:
+        _call_on(pool.get_device(), "decode_attn_read_paged_quant", stream, pool.data_ptr(),
+                 slot_mapping.data_ptr(), k_out.data_ptr(), v_out.data_ptr(), T, Hkv, D, P,
+                 pool.shape[0], bits, group)
     return k_out, v_out
 
 
@@ -383,28 +403,30 @@ def decode_attn_paged_quant(q, pool, out, block_table, kv_lens, kv_len_stride: i
     """q, out [B,Hq,Sq,D] bf16; a quantised pool [num_pages,Hkv,page_bytes]; block table and
     lengths as for decode_attn_paged.  Workspace: decode_attn_workspace_size(
     DA_VARIANT_PAGED_QUANT, B, Hq * Sq, Hkv, D)."""
-    B, Hq, Sq, D = q.shape
+    shape = q.shape
+    B, Hq, Sq, D = shape
     P = _quant_page_size(pool, D, bits, group)
-    dev = pool.device
-    _want(q, "q", torch.bfloat16, 4, dev)
-    _want(out, "out", torch.bfloat16, 4, dev)
-    _want(block_table, "block_table", torch.int32, 2, dev)
-    if out.shape != q.shape or block_table.shape[0] != B:
-        raise ValueError("out must have q's shape and block_table a row per sequence")
-    if not kv_lens.is_contiguous() or kv_lens.device != dev or kv_lens.element_size() != 4 or \
+    dev = pool.get_device()
+    if q.dtype != torch.bfloat16 or not q.is_contiguous() or q.get_device() != dev:
+        _refuse(f"q must be contiguous bf16 on {pool.device}")
+    if out.dtype != torch.bfloat16 or not out.is_contiguous() or out.get_device() != dev or \
+            out.shape != shape:
+        _refuse(f"out must be contiguous bf16 of q's shape on {pool.device}")
+    if block_table.dtype != torch.int32 or block_table.dim() != 2 or \
+            not block_table.is_contiguous() or block_table.get_device() != dev or \
+            block_table.shape[0] != B:
+        _refuse(f"block_table must be contiguous int32 [{B}, pages] on {pool.device}")
+    if kv_lens.get_device() != dev or not kv_lens.is_contiguous() or kv_lens.element_size() != 4 or \
             kv_lens.numel() < (B - 1) * kv_len_stride + 1:
-        raise ValueError("kv_lens must hold a 32-bit length per sequence on the pool's device")
-    if workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous buffer on the pool's device")
-    if q.numel() == 0:
-        return out
-    with _on(dev):
-        _check(load_library().decode_attn_paged_quant(
-            _ptr(q), _ptr(pool), _ptr(out), _ptr(block_table), block_table.shape[1], P,
-            pool.shape[0], _ptr(kv_lens), int(kv_len_stride), B, Hq, pool.shape[1], D, Sq,
-            int(bool(causal)), int(bits), int(group), float(softmax_scale), _ptr(workspace),
-            workspace.numel() * workspace.element_size(), _stream(stream, dev)),
-            "decode_attn_paged_quant")
+        _refuse(f"kv_lens must hold a contiguous 32-bit length per sequence on {pool.device}")
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        _refuse(f"workspace must be a contiguous buffer on {pool.device}")
+    if q.numel():
+        _call_on(dev, "decode_attn_paged_quant", stream, q.data_ptr(), pool.data_ptr(),
+                 out.data_ptr(), block_table.data_ptr(), block_table.shape[1], P, pool.shape[0],
+                 kv_lens.data_ptr(), kv_len_stride, B, Hq, pool.shape[1], D, Sq, bool(causal),
+                 bits, group, softmax_scale, workspace.data_ptr(),
+                 workspace.numel() * workspace.element_size())
     return out
 
 

@@ -190,12 +190,18 @@ int paged_kv_heads(int Hkv, int G, int page_size) {
 constexpr long long kShortUnitTiles = 8;
 
 // Quantised paged units: warps that split a KV head's `cols` query columns (log2), and the KV heads
-// per unit for that many -- the most (a power of two dividing Hkv) that still leave each head a warp
-// of every eight.
+// per unit: the most (a power of two dividing Hkv) that leave each head a warp of every group of
+// consumer warps and still give units for 80% of the SMs, one otherwise.  More heads per unit make
+// fewer and larger copies and fewer segment ends (64 ragged sequences of 8 KV heads: 181 us with four
+// heads a unit, 187 with two, 199 with one); fewer spread the merges of split units over more CTAs
+// (16 sequences of 4096 rows: 22.0 us with one, 22.9 with two, 25.7 with four).
 int quant_slices_shift(int cols) { return cols <= 16 ? 0 : cols <= 32 ? 1 : 2; }
-int quant_kv_heads(int Hkv, int cols) {
+int quant_kv_heads(int B, int Hkv, int cols, int bits, int sms) {
+    const int warps = bits == 4 && cols <= 8 ? 4 : 8;
     int kh = 1;
-    while (Hkv % (2 * kh) == 0 && (2 * kh << quant_slices_shift(cols)) <= 8) kh *= 2;
+    while (Hkv % (2 * kh) == 0 && (2 * kh << quant_slices_shift(cols)) <= warps &&
+           5ll * B * (Hkv / (2 * kh)) >= 4ll * sms)
+        kh *= 2;
     return kh;
 }
 
@@ -301,8 +307,11 @@ size_t decode_attn_workspace_size(int variant, int B, int Hq, int Hkv, int D, in
         const int sms = sm_count(dev);
         if (sms <= 0) return 0;
         if (variant == DA_VARIANT_PAGED_QUANT) {
-            const int kh = quant_kv_heads(Hkv, G);
-            return ws_layout(units / kh, units / kh + sms, kh * G, D).total;
+            // the number of bits is not an argument here: size for every unit width a call may use
+            size_t most = 0;
+            for (int kh = 1; kh <= 8 && Hkv % kh == 0; kh *= 2)
+                most = std::max(most, ws_layout(units / kh, units / kh + sms, kh * G, D).total);
+            return most;
         }
         if (variant == DA_VARIANT_PAGED) {
             // the page size is not an argument here: size for every unit width a call may use
@@ -663,7 +672,7 @@ extern "C" da_status decode_attn_paged_quant(
     if (sms <= 0) return DA_ERR_CUDA;
     QuantParams p{};
     p.cols = (Hq / Hkv) * Sq;
-    p.kh = quant_kv_heads(Hkv, p.cols);
+    p.kh = quant_kv_heads(B, Hkv, p.cols, bits, sms);
     const long long qunits = units / p.kh;
     const WsLayout w = ws_layout(qunits, qunits + sms, p.kh * p.cols, D);
     if (workspace_bytes < w.total) return DA_ERR_WORKSPACE_TOO_SMALL;

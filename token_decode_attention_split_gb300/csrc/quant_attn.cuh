@@ -16,13 +16,29 @@
 // x_j + log2 vs_j, and f = 2^(m - M).  Both are raised only when a weight passes 2^8, so the usual
 // tile has no cross-lane maximum at all; sums stay in fp32 and are exact in the reference.
 //
-// Work.  A unit is one sequence and kh adjacent KV heads; a stage is kTileRows-row tiles of every
-// one of those heads.  The stages of all units are laid end to end and CTA c of a persistent grid
+// V's codes are taken about their middle code: sum w c = sum w (c - mid) + mid sum w, the second sum
+// in fp32 (it joins vmin) and the first as the product minus mid times the sum of the rounded weights
+// (one more MMA per tile, whose A operand is mid everywhere), so a weight's rounding error meets
+// centred codes.  At 131071 keys the output's error falls from 0.0030 to 0.0018 of its norm (its own
+// bf16 rounding is 0.0017).
+//
+// Work.  A unit is one sequence and kh adjacent KV heads; a stage is 128 or 256 rows, split evenly
+// over those heads.  The stages of all units are laid end to end and CTA c of a persistent grid
 // (one per SM) takes an equal contiguous range; its piece of a unit is a segment.  A page of kh
-// heads is contiguous (codes and parameters), so a stage is a few bulk copies.  One warp copies
-// into a ring of stages, the others each take 16-row tiles of one KV head: S^T = K Q^T and
-// O^T += V^T P^T on mma.m16n8k16 with the keys (then the elements of V) on M and the query columns
-// on N, and own running state per warp, merged once per segment.
+// heads is contiguous (codes and parameters), so a stage is a few bulk copies.  The warps of a copying
+// warpgroup fill a ring of stages; consumer warps each take 16-row tiles of one KV head: S^T = K Q^T
+// and O^T += V^T P^T on mma.m16n8k16 with the keys (then the elements of V) on M and the query columns
+// on N, each with a running state of its own, merged once per segment.
+//
+// What bounds it.  8-bit codes: HBM.  4-bit codes halve the bytes and leave 48 ns of HBM time per
+// 16-row tile and SM (D = 128, 136 bytes a row) for about 200 warp instructions, 104 of them the masks,
+// shifts and byte permutes that make fp16 operands (two cycles each on their pipe): the kernel is issue
+// bound at about 56 ns a tile (measured with the cache in L2), so everything around the tiles is kept
+// off the schedulers.  Twelve consumer warps of 160 registers in three groups, each on every third
+// stage, and three copying warps: 64 ns a tile (66 with eight consumer warps in one group, 71 with
+// sixteen of 112 registers; 74 with one copying warp, whose lookup, wait and copy take longer than a
+// stage); fp32 arithmetic on register pairs (f32x2) and waits that nap instead of polling: 62 ns; warp
+// indices broadcast, so that no warp-wide instruction needs a convergence check: 56 ns.
 //
 // A segment that covers its unit writes the output; any other writes its normalised partial rows
 // and log2-sum-exps, and the CTA that completes the unit (an acquire-release counter) merges them
@@ -66,35 +82,56 @@ struct QuantGeometry {
     static constexpr int PB = kQuantRowParams(D, D / NG);
     static constexpr int ROW = 2 * RB + PB;
     static constexpr int NT = NC / 8;                      // 8-column n-tiles of a warp
-    static constexpr int W = 8;                             // consumer warps
+    // Consumer warps work in groups, each group on its own stage in turn.
+    static constexpr bool kNarrow4 = NC == 8 && BITS == 4;
+    static constexpr int kGroups = kNarrow4 ? 3 : 1;
+    static constexpr int WG = kNarrow4 ? 4 : 8;            // warps of a group
+    static constexpr int W = kGroups * WG;
     static constexpr int kConsumers = 32 * W;
-    static constexpr int kThreads = kConsumers + 32;       // and one copying warp
-    static constexpr int kTiles = (D == 128 && BITS == 8) ? 8 : 16;   // 16-row tiles of a stage
+    // Copying warps (of one more warpgroup), each on every kCopyWarps-th stage.  The ring has a multiple
+    // of kGroups and of kCopyWarps slots, so a slot is always filled by the same warp and emptied by
+    // the same group: nobody can wait for a phase two rounds away, which a parity could not tell from
+    // the one before.
+    static constexpr int kCopyWarps = kGroups;
+    static constexpr int kThreads = kConsumers + 128;
+    // Registers per thread: the launch gives every thread the same share of 65536; the copying
+    // warpgroup hands most of its own to the consumers.
+    static constexpr int kLaunchRegs = kNarrow4 ? 128 : 168;
+    static constexpr int kCopyRegs = kNarrow4 ? 32 : 40;
+    static constexpr int kConsumerRegs = kNarrow4 ? 160 : 232;
+    static_assert(kConsumers * kConsumerRegs + 128 * kCopyRegs <= kThreads * kLaunchRegs, "registers");
+    static constexpr int kTiles = kNarrow4 || (D == 128 && BITS == 8) ? 8 : 16;   // 16-row tiles of a stage
+    static constexpr int UT = NC == 8 && NG < 4 ? kTiles / WG : 1;   // tiles that a warp takes together
+    static constexpr int TPW = NC == 8 ? kTiles / WG / UT : 1;   // sets of them whose places are kept
     static constexpr int kStageRows = kTiles * 16;
     static constexpr int kStageBytes = kStageRows * ROW;
     static constexpr int kMergeStride = D + 4;             // floats of a merge row
-    static constexpr int kMergeFloats = 8 * 8 * kMergeStride + 2 * 8 * 8;
+    static constexpr int kMergeFloats = W * NC * (kMergeStride + 2);   // [warp][column]
+    static constexpr int kMaxStages = kGroups == 3 ? 9 : 8;
     static constexpr int kMiscBytes = 512;
     static constexpr int kSchedBytes = (2 * kMaxPagedBatch + 2) * 4;
     static constexpr int kFixedBytes = kMergeFloats * 4 + kMiscBytes + kSchedBytes;
     static constexpr int kStagesFit = (kSmemBudget - 128 - kFixedBytes) / kStageBytes;
-    static constexpr int kStages = kStagesFit > 8 ? 8 : kStagesFit;
+    static constexpr int kStages =
+        (kStagesFit > kMaxStages ? kMaxStages : kStagesFit) / kCopyWarps * kCopyWarps;
     static constexpr int kSmemBytes = 128 + kStages * kStageBytes + kFixedBytes;
-    static_assert(kStages >= 2 && kStageBytes % 128 == 0 && kTiles >= W, "ring");
+    static_assert(kStages >= kCopyWarps && kStages >= 2 && kStages % kCopyWarps == 0 && kStages % kGroups == 0 && kStageBytes % 128 == 0 && kTiles >= WG, "ring");
 };
 
 struct QuantSmem {
     unsigned char* stages;
-    float* merge_o;      // [8 warps][8 columns][kMergeStride]
-    float* merge_m;      // [8][8]
-    float* merge_l;      // [8][8]
+    float* merge_o;      // [W][NC columns][kMergeStride]
+    float* merge_m;      // [W][NC]
+    float* merge_l;      // [W][NC]
     uint64_t* full;
     uint64_t* empty;
-    uint64_t* group;
-    unsigned* stage_len;     // rows per head of the stage that lie inside the sequence
+    uint64_t* group;         // all consumers
+    uint64_t* stashed;       // the merge slots hold every warp's columns of this round
+    uint64_t* combined;      // they have been merged and may be written again
+    int* stage_len;          // rows per head of the stage inside the sequence; -1: every row counts
     unsigned* stage_pages;   // bit i: page i of the stage was copied
     volatile int* abort;
-    int* last_flag;
+    int* last_flag;      // [2]
     int* seq_prefix;     // [B + 1] exclusive prefix of the sequences' stages
     int* seq_len;        // [B]
 };
@@ -106,17 +143,19 @@ __device__ __forceinline__ QuantSmem quant_carve(unsigned char* raw) {
     s.stages = base;
     unsigned char* p = base + Gm::kStages * Gm::kStageBytes;
     s.full = reinterpret_cast<uint64_t*>(p);
-    s.empty = s.full + 8;
-    s.group = s.empty + 8;
-    s.stage_len = reinterpret_cast<unsigned*>(s.group + 1);
-    s.stage_pages = s.stage_len + 8;
-    s.abort = reinterpret_cast<volatile int*>(s.stage_pages + 8);
+    s.empty = s.full + Gm::kMaxStages;
+    s.group = s.empty + Gm::kMaxStages;
+    s.stashed = s.group + 1;
+    s.combined = s.stashed + 1;
+    s.stage_len = reinterpret_cast<int*>(s.combined + 1);
+    s.stage_pages = reinterpret_cast<unsigned*>(s.stage_len + Gm::kMaxStages);
+    s.abort = reinterpret_cast<volatile int*>(s.stage_pages + Gm::kMaxStages);
     s.last_flag = const_cast<int*>(s.abort) + 1;
     p += Gm::kMiscBytes;
     s.merge_o = reinterpret_cast<float*>(p);
-    s.merge_m = s.merge_o + 8 * 8 * Gm::kMergeStride;
-    s.merge_l = s.merge_m + 64;
-    s.seq_prefix = reinterpret_cast<int*>(s.merge_l + 64);
+    s.merge_m = s.merge_o + Gm::W * Gm::NC * Gm::kMergeStride;
+    s.merge_l = s.merge_m + Gm::W * Gm::NC;
+    s.seq_prefix = reinterpret_cast<int*>(s.merge_l + Gm::W * Gm::NC);
     s.seq_len = s.seq_prefix + kMaxPagedBatch + 1;
     return s;
 }
@@ -145,9 +184,42 @@ __device__ __forceinline__ QuantUnit quant_locate(const QuantParams& p, const Qu
     return U;
 }
 
+// The unit after U (one exists): the next head group, or the next sequence with rows.
+__device__ __forceinline__ QuantUnit quant_next(const QuantParams& p, const QuantSmem& sm, QuantUnit U) {
+    U.base += U.nt;
+    ++U.u;
+    if (++U.g == p.Hkv / p.kh) {
+        U.g = 0;
+        do {
+            ++U.b;
+            U.nt = sm.seq_prefix[U.b + 1] - sm.seq_prefix[U.b];
+            if (U.nt == 0) U.u += p.Hkv / p.kh;
+        } while (U.nt == 0);
+        U.len = sm.seq_len[U.b];
+    }
+    return U;
+}
+
+// mbar_wait_warp that naps between its polls, so that a waiting warp leaves the scheduler's issue slots
+// to the others (the twelve consumer warps of the 4-bit kernel are bound by them).
+// Gives up after about a second of naps, or when another thread of the CTA has raised *abort.
+template <unsigned NAP_NS>
+__device__ __forceinline__ bool quant_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+    bool done = mbar_try_wait(bar, parity);
+    if (!__all_sync(0xffffffffu, done)) {
+        for (unsigned polls = 0; !done && !*abort && polls < kWaitLimitNs / NAP_NS; ++polls) {
+            __nanosleep(NAP_NS);
+            done = mbar_try_wait(bar, parity);
+        }
+        done = __all_sync(0xffffffffu, done);
+    }
+    return done;
+}
+constexpr unsigned kNapConsumer = 40, kNapCopy = 200, kNapGroup = 20;
+
 __device__ __forceinline__ bool quant_sync(const QuantSmem& sm, uint32_t& phase, unsigned* err) {
     mbar_arrive(sm.group);
-    const bool ok = mbar_wait_warp(sm.group, phase, sm.abort);
+    const bool ok = quant_wait<kNapGroup>(sm.group, phase, sm.abort);
     phase ^= 1u;
     if (!ok) {
         *sm.abort = 1;
@@ -166,25 +238,68 @@ __device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// D = A * B
+__device__ __forceinline__ void mma_f16_16816_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                                    uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
+        "{%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     __half2 v = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<uint32_t*>(&v);
 }
 
-// N consecutive words of shared memory at `addr` (aligned to their size, at most 16 bytes a load)
+// N consecutive words (aligned to their size, at most 16 bytes a load)
 template <int N>
-__device__ __forceinline__ void lds(uint32_t addr, uint32_t (&r)[N]) {
+__device__ __forceinline__ void lds(const unsigned char* at, uint32_t (&r)[N]) {
     if constexpr (N == 1) {
-        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r[0]) : "r"(addr));
+        r[0] = *reinterpret_cast<const uint32_t*>(at);
     } else if constexpr (N == 2) {
-        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(addr));
+        const uint2 x = *reinterpret_cast<const uint2*>(at);
+        r[0] = x.x;
+        r[1] = x.y;
     } else {
 #pragma unroll
-        for (int i = 0; i < N; i += 4)
-            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3])
-                         : "r"(addr + 4 * i));
+        for (int i = 0; i < N; i += 4) {
+            const uint4 x = *reinterpret_cast<const uint4*>(at + 4 * i);
+            r[i] = x.x;
+            r[i + 1] = x.y;
+            r[i + 2] = x.z;
+            r[i + 3] = x.w;
+        }
     }
+}
+
+// Two fp32 numbers in a register pair and the packed arithmetic on them (one instruction for both).
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 f2_of(float lo, float hi) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float f2_get(f2 v, int i) {
+    float lo, hi;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+    return i ? hi : lo;
+}
+__device__ __forceinline__ f2 f2_fma(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f2 f2_mul(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 f2_add(f2 a, f2 b) {
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
 }
 
 // Row of a 16-row tile (0..7; +8 for the second half) that stands at fragment row i: neighbouring
@@ -196,7 +311,7 @@ constexpr float kQuantUnset = -3.402823466e38f;   // reference of a column that 
 
 template <class Gm>
 struct QuantWarp {
-    static constexpr int D = Gm::D, BITS = Gm::BITS, NG = Gm::NG, NT = Gm::NT;
+    static constexpr int D = Gm::D, BITS = Gm::BITS, NG = Gm::NG, NT = Gm::NT, UT = Gm::UT;
     static constexpr int S = D / 16;             // 16-element slices: MMA k-steps of a K row, m-tiles of V
     static constexpr int KW = Gm::RB / 16;       // words of a K row per lane
     static constexpr int VW = Gm::RB / 32;       // words of a V row per lane
@@ -204,36 +319,39 @@ struct QuantWarp {
     // powers of two of the code operands: 2^-24, and 2^-20 for the upper codes of the 4-bit pairs
     static constexpr float kUnit = 16777216.f;
     static constexpr float kUnitHi = BITS == 4 ? 1048576.f : 16777216.f;
+    // the middle code, taken off the V codes again (see the file's head), and as code operands
+    static constexpr int kMid = BITS == 4 ? 8 : 128;
+    static constexpr uint32_t kMidLo = kMid * 0x00010001u, kMidHi = (BITS == 4 ? 16 : 1) * kMidLo;
 
     int lane, gq, qd;                // fragment row, quad lane
     int head, col0;                  // KV head of the unit, first query column
     uint32_t qf[S][NT][2];           // Q^T fragments (fp16, scaled by a power of two per column)
-    float qsum[NG][NT][2];           // sum of a column's scaled elements per group, in code units
-    float cf[NT][2];                 // score units -> log2 domain
+    // pairs: columns 2 qd and 2 qd + 1 of an n-tile
+    f2 qsum[NG][NT];                 // sum of a column's scaled elements per group, in code units
+    f2 cf[NT];                       // score units -> log2 domain
     float o[S][NT][4];               // O^T: rows gq (element 16 m + 2 gq) and gq + 8 (element + 1)
-    float z[NG][NT][2];              // this lane's share of sum p * vmin
-    float l[NT][2];                  // this lane's share of sum p
-    float m[NT][2], M[NT][2], f[NT][2];
+    f2 z[NG][NT];                    // this lane's share of sum p * (vmin + kMid * vs)
+    float w0[NG][NT][4];             // kMid * sum of the fp16 weights, in o's units
+    f2 l[NT];                        // this lane's share of sum p
+    f2 nm[NT], f[NT];                // -m and 2^(m - M)
+    float M[NT][2];
     int tok[NT][2];                  // query token of the column (causal)
-    uint32_t koff[2], voff[4], poff[2];   // lane offsets inside a tile: K rows, V rows, parameters
+    int koff, voff[2], poff;         // lane offsets inside a tile: K row, V rows, parameters
+    int half_k, half_p;              // from a row of the tile's first half to its second half
 
-    __device__ __forceinline__ void init(int lane_, int head_, int col0_, int sq, int half_k,
-                                         int half_p) {
+    __device__ __forceinline__ void init(int lane_, int head_, int col0_, int sq, int half_k_,
+                                         int half_p_) {
         lane = lane_;
         gq = lane >> 2;
         qd = lane & 3;
         head = head_;
         col0 = col0_;
-        const int r = quant_tile_row(gq);
-        const int ra = quant_tile_row(2 * qd), rb = quant_tile_row(2 * qd + 1);
-        koff[0] = r * Gm::RB + qd * (4 * KW);
-        koff[1] = koff[0] + half_k;
-        voff[0] = ra * Gm::RB + gq * (4 * VW);
-        voff[1] = rb * Gm::RB + gq * (4 * VW);
-        voff[2] = voff[0] + half_k;
-        voff[3] = voff[1] + half_k;
-        poff[0] = r * Gm::PB;
-        poff[1] = poff[0] + half_p;
+        koff = quant_tile_row(gq) * Gm::RB + qd * (4 * KW);
+        voff[0] = quant_tile_row(2 * qd) * Gm::RB + gq * (4 * VW);
+        voff[1] = quant_tile_row(2 * qd + 1) * Gm::RB + gq * (4 * VW);
+        poff = quant_tile_row(gq) * Gm::PB;
+        half_k = half_k_;
+        half_p = half_p_;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -248,29 +366,39 @@ struct QuantWarp {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[i][nt][e] = 0.f;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt) {
+            l[nt] = f2_of(0.f, 0.f);
+            nm[nt] = f2_of(-kQuantUnset, -kQuantUnset);
+            f[nt] = f2_of(1.f, 1.f);
+            M[nt][0] = M[nt][1] = kQuantUnset;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                l[nt][e] = 0.f;
-                m[nt][e] = M[nt][e] = kQuantUnset;
-                f[nt][e] = 1.f;
+            for (int g = 0; g < NG; ++g) {
+                z[g][nt] = f2_of(0.f, 0.f);
 #pragma unroll
-                for (int g = 0; g < NG; ++g) z[g][nt][e] = 0.f;
+                for (int e = 0; e < 4; ++e) w0[g][nt][e] = 0.f;
             }
+        }
     }
 
-    // Query rows row0 .. row0 + cols - 1 (columns at or past cols are zero)
-    __device__ __forceinline__ void load_q(const QuantParams& p, size_t row0) {
+    // Query rows row0 .. row0 + cols - 1 (columns at or past cols are zero): elements 16 s + 4 qd .. + 3
+    // of column gq of each n-tile
+    __device__ __forceinline__ void fetch_q(const QuantParams& p, size_t row0, uint2 (&raws)[NT][S]) const {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int c = col0 + nt * 8 + gq;
             const bool ok = c < p.cols;
             const uint2* row = reinterpret_cast<const uint2*>(p.q + (row0 + (ok ? c : 0)) * D);
-            uint2 raw[S];                 // elements 16 s + 4 qd .. + 3
+#pragma unroll
+            for (int s = 0; s < S; ++s) raws[nt][s] = ok ? __ldg(row + 4 * s + qd) : make_uint2(0u, 0u);
+        }
+    }
+    __device__ __forceinline__ void set_q(float scale_log2, const uint2 (&raws)[NT][S]) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const uint2(&raw)[S] = raws[nt];
             uint32_t top = 0;
 #pragma unroll
             for (int s = 0; s < S; ++s) {
-                raw[s] = ok ? __ldg(row + 4 * s + qd) : make_uint2(0u, 0u);
                 top = max(top, max((raw[s].x << 16) & 0x7fffffffu, raw[s].x & 0x7fff0000u));
                 top = max(top, max((raw[s].y << 16) & 0x7fffffffu, raw[s].y & 0x7fff0000u));
             }
@@ -316,271 +444,318 @@ struct QuantWarp {
                 x += __shfl_xor_sync(0xffffffffu, x, 1);
                 x += __shfl_xor_sync(0xffffffffu, x, 2);
                 x *= 1.f / kUnit;
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    qsum[g][nt][e] = __shfl_sync(0xffffffffu, x, (2 * qd + e) * 4);
+                qsum[g][nt] = f2_of(__shfl_sync(0xffffffffu, x, 8 * qd), __shfl_sync(0xffffffffu, x, 8 * qd + 4));
             }
-            const float c2 = p.scale_log2 * down * kUnit;
-#pragma unroll
-            for (int e = 0; e < 2; ++e) cf[nt][e] = __shfl_sync(0xffffffffu, c2, (2 * qd + e) * 4);
+            const float c2 = scale_log2 * down * kUnit;
+            cf[nt] = f2_of(__shfl_sync(0xffffffffu, c2, 8 * qd), __shfl_sync(0xffffffffu, c2, 8 * qd + 4));
         }
     }
 
-    // Raises the references to the maxima of this tile (and of all tiles before).
-    __device__ __forceinline__ void raise(const float (&x)[NT][4], const float (&ls)[2]) {
+    // Raises the references to the maxima of these tiles (and of all tiles before).  x: scores before
+    // the factor cf; ls: log2 of a row's largest scale; hidden(u, nt, e): the element does not count.
+    template <class Hidden>
+    __device__ __forceinline__ void raise(const f2 (&x)[UT][NT][2], const float (&ls)[UT][2], Hidden hidden) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt) {
+            float al[2], ao[2], nf[2], nn[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                float a = fmaxf(x[nt][e], x[nt][e + 2]);
-                float b = fmaxf(x[nt][e] + ls[0], x[nt][e + 2] + ls[1]);
+                const float c = f2_get(cf[nt], e), m = -f2_get(nm[nt], e);
+                float a = m, b = M[nt][e];
+#pragma unroll
+                for (int u = 0; u < UT; ++u)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        if (hidden(u, nt, e + 2 * i)) continue;
+                        const float y = f2_get(x[u][nt][i], e);
+                        a = fmaxf(a, y * c);
+                        b = fmaxf(b, __fmaf_rn(y, c, ls[u][i]));
+                    }
 #pragma unroll
                 for (int off = 4; off < 32; off *= 2) {
                     a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
                     b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, off));
                 }
-                a = fmaxf(a, m[nt][e]);
-                b = fmaxf(b, M[nt][e]);
-                const float al = fast_exp2(m[nt][e] - a), ao = fast_exp2(M[nt][e] - b);
-                m[nt][e] = a;
+                al[e] = fast_exp2(m - a);
+                ao[e] = fast_exp2(M[nt][e] - b);
+                nf[e] = fast_exp2(a - b);
+                nn[e] = -a;
                 M[nt][e] = b;
-                f[nt][e] = fast_exp2(a - b);
-                l[nt][e] *= al;
 #pragma unroll
-                for (int g = 0; g < NG; ++g) z[g][nt][e] *= al;
+                for (int g = 0; g < NG; ++g) {
+                    w0[g][nt][e] *= ao[e];
+                    w0[g][nt][e + 2] *= ao[e];
+                }
 #pragma unroll
                 for (int i = 0; i < S; ++i) {
-                    o[i][nt][e] *= ao;
-                    o[i][nt][e + 2] *= ao;
+                    o[i][nt][e] *= ao[e];
+                    o[i][nt][e + 2] *= ao[e];
                 }
             }
+            nm[nt] = f2_of(nn[0], nn[1]);
+            f[nt] = f2_of(nf[0], nf[1]);
+            const f2 al2 = f2_of(al[0], al[1]);
+            l[nt] = f2_mul(l[nt], al2);
+#pragma unroll
+            for (int g = 0; g < NG; ++g) z[g][nt] = f2_mul(z[g][nt], al2);
+        }
     }
 
-    // One 16-row tile at shared-memory addresses k, v, par (row 0 of the tile's first half).
-    // MASKED: bit r of rows = row r of the tile counts, and column c sees keys up to last + tok[c].
+    // This lane's places in a tile whose K codes, V codes and parameters begin at byte k, v, par of a
+    // stage: its K row, the V rows of its two keys, its parameters (those of the tile's second half
+    // lie half_k and half_p further).
+    struct TileAt {
+        int k, va, vb, par;
+    };
+    __device__ __forceinline__ TileAt tile_at(int k, int v, int par) const {
+        return {k + koff, v + voff[0], v + voff[1], par + poff};
+    }
+
+    // UT 16-row tiles of one KV head in a stage.
+    // MASKED: bit r of rows[u] = row r of the tile counts, and column c sees keys up to last + tok[c].
     template <bool MASKED>
-    __device__ __forceinline__ void tile(uint32_t k, uint32_t v, uint32_t par, uint32_t rows,
-                                         int key0, int last) {
-        uint32_t ka[KW], kb[KW], pa[PW], pb_[PW];
-        lds<KW>(k + koff[0], ka);
-        lds<KW>(k + koff[1], kb);
-        lds<PW>(par + poff[0], pa);
-        lds<PW>(par + poff[1], pb_);
-        float x[NT][4];
+    __device__ __forceinline__ void tiles(const unsigned char* stage, const TileAt (&at)[UT],
+                                          const uint32_t (&rows)[UT], const int (&key0)[UT], int last) {
+        // from a row to the one 8 further: a constant unless pages have 8 rows, whose stages always come
+        // masked
+        const int hk = MASKED ? half_k : 8 * Gm::RB, hp = MASKED ? half_p : 8 * Gm::PB;
+        uint32_t pa[UT][2][PW];           // parameters of the rows at gq and at gq + 8
+        f2 x[UT][NT][2];                  // scores before the factor cf, the same rows
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
-            float acc[NT][4];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[nt][e] = 0.f;
-#pragma unroll
-            for (int w = g * KW / NG; w < (g + 1) * KW / NG; ++w) {
-                if constexpr (BITS == 4) {
-                    const uint32_t a8 = ka[w] >> 8, b8 = kb[w] >> 8;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint32_t mask = h ? 0x00f000f0u : 0x000f000fu;
-                        const uint32_t a0 = ka[w] & mask, a1 = kb[w] & mask, a2 = a8 & mask,
-                                       a3 = b8 & mask;
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-                            mma_f16_16816(acc[nt], a0, a1, a2, a3, qf[2 * w + h][nt][0],
-                                          qf[2 * w + h][nt][1]);
-                    }
-                } else {
-                    const uint32_t a0 = __byte_perm(ka[w], 0u, 0x4140), a1 = __byte_perm(kb[w], 0u, 0x4140),
-                                   a2 = __byte_perm(ka[w], 0u, 0x4342), a3 = __byte_perm(kb[w], 0u, 0x4342);
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        mma_f16_16816(acc[nt], a0, a1, a2, a3, qf[w][nt][0], qf[w][nt][1]);
-                }
-            }
-            const float sa = bf16_lo_to_f32(pa[2 * g]), na = bf16_hi_to_f32(pa[2 * g]);
-            const float sb = bf16_lo_to_f32(pb_[2 * g]), nb = bf16_hi_to_f32(pb_[2 * g]);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float y = (e < 2 ? na : nb) * qsum[g][nt][e & 1];
-                    const float base = g == 0 ? y : y + x[nt][e];
-                    x[nt][e] = __fmaf_rn(e < 2 ? sa : sb, acc[nt][e], base);
-                }
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[nt][e] *= cf[nt][e & 1];
-
-        float vsa[NG], vsb[NG], vna[NG], vnb[NG];
-#pragma unroll
-        for (int g = 0; g < NG; ++g) {
-            vsa[g] = bf16_lo_to_f32(pa[2 * g + 1]);
-            vna[g] = bf16_hi_to_f32(pa[2 * g + 1]);
-            vsb[g] = bf16_lo_to_f32(pb_[2 * g + 1]);
-            vnb[g] = bf16_hi_to_f32(pb_[2 * g + 1]);
-        }
-        if constexpr (MASKED) {
-            // rows that do not count may hold anything, NaN parameters too
-            const int r = quant_tile_row(gq);
-            const bool oka = (rows >> r) & 1u, okb = (rows >> (r + 8)) & 1u;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int key = key0 + r + (e < 2 ? 0 : 8);
-                    if (!(e < 2 ? oka : okb) || key - tok[nt][e & 1] > last) x[nt][e] = -CUDART_INF_F;
-                }
+        for (int u = 0; u < UT; ++u) {
+            uint32_t ka[KW], kb[KW];
+            lds<KW>(stage + at[u].k, ka);
+            lds<KW>(stage + at[u].k + hk, kb);
+            lds<PW>(stage + at[u].par, pa[u][0]);
+            lds<PW>(stage + at[u].par + hp, pa[u][1]);
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
-                if (!oka) vsa[g] = vna[g] = 0.f;
-                if (!okb) vsb[g] = vnb[g] = 0.f;
-            }
-        }
-
-        // weights: p for the sums, p * f * vs for the product
-        float pe[NT][4], wt[NG][NT][4], top;
-        auto weights = [&]() {
-            top = 0.f;
+                float acc[NT][4];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+                for (int w = g * KW / NG; w < (g + 1) * KW / NG; ++w) {
+                    const bool first = w == g * KW / NG;
+                    if constexpr (BITS == 4) {
+                        const uint32_t a8 = ka[w] >> 8, b8 = kb[w] >> 8;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    pe[nt][e] = fast_exp2(x[nt][e] - m[nt][e & 1]);
-                    top = fmaxf(top, pe[nt][e]);
-                    const float pf = pe[nt][e] * f[nt][e & 1];
+                        for (int h = 0; h < 2; ++h) {
+                            const uint32_t mask = h ? 0x00f000f0u : 0x000f000fu;
+                            const uint32_t a0 = ka[w] & mask, a1 = kb[w] & mask, a2 = a8 & mask,
+                                           a3 = b8 & mask;
 #pragma unroll
-                    for (int g = 0; g < NG; ++g) {
-                        wt[g][nt][e] = pf * (e < 2 ? vsa[g] : vsb[g]);
-                        // a key that the column does not see adds nothing, whatever its row holds
-                        if (MASKED && x[nt][e] == -CUDART_INF_F) wt[g][nt][e] = 0.f;
-                        top = fmaxf(top, wt[g][nt][e]);
+                            for (int nt = 0; nt < NT; ++nt) {
+                                if (first && h == 0)
+                                    mma_f16_16816_first(acc[nt], a0, a1, a2, a3, qf[2 * w][nt][0],
+                                                        qf[2 * w][nt][1]);
+                                else
+                                    mma_f16_16816(acc[nt], a0, a1, a2, a3, qf[2 * w + h][nt][0],
+                                                  qf[2 * w + h][nt][1]);
+                            }
+                        }
+                    } else {
+                        const uint32_t a0 = __byte_perm(ka[w], 0u, 0x4140),
+                                       a1 = __byte_perm(kb[w], 0u, 0x4140),
+                                       a2 = __byte_perm(ka[w], 0u, 0x4342),
+                                       a3 = __byte_perm(kb[w], 0u, 0x4342);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            if (first)
+                                mma_f16_16816_first(acc[nt], a0, a1, a2, a3, qf[w][nt][0], qf[w][nt][1]);
+                            else
+                                mma_f16_16816(acc[nt], a0, a1, a2, a3, qf[w][nt][0], qf[w][nt][1]);
+                        }
                     }
                 }
-        };
-        weights();
-        if (__any_sync(0xffffffffu, top > 256.f)) {
-            float sa = vsa[0], sb = vsb[0];
 #pragma unroll
-            for (int g = 1; g < NG; ++g) {
-                sa = fmaxf(sa, vsa[g]);
-                sb = fmaxf(sb, vsb[g]);
-            }
-            // a scale's exponent within [-64, 120]: 0 has none, and 2^(m - M) stays a normal number
-            const float ls[2] = {fminf(fmaxf(fast_log2(sa), -64.f), 120.f),
-                                 fminf(fmaxf(fast_log2(sb), -64.f), 120.f)};
-            raise(x, ls);
-            weights();
-        }
-        uint32_t pb[NG][NT][2];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            l[nt][0] += pe[nt][0] + pe[nt][2];
-            l[nt][1] += pe[nt][1] + pe[nt][3];
-#pragma unroll
-            for (int g = 0; g < NG; ++g) {
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float za = pe[nt][e] * vna[g], zb = pe[nt][e + 2] * vnb[g];
-                    if (MASKED && x[nt][e] == -CUDART_INF_F) za = 0.f;
-                    if (MASKED && x[nt][e + 2] == -CUDART_INF_F) zb = 0.f;
-                    z[g][nt][e] += za + zb;
-                }
-                pb[g][nt][0] = movmatrix_trans(pack_f16x2(wt[g][nt][0], wt[g][nt][1]));
-                pb[g][nt][1] = movmatrix_trans(pack_f16x2(wt[g][nt][2], wt[g][nt][3]));
-            }
-        }
-
-        // O^T += V^T P^T: pairs of keys for one element from the words of two rows
-        uint32_t va[4][VW];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) lds<VW>(v + voff[i], va[i]);
-#pragma unroll
-        for (int w = 0; w < VW; ++w)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const uint32_t sel = h ? 0x7632u : 0x5410u;
-                const uint32_t lo = __byte_perm(va[0][w], va[1][w], sel);
-                const uint32_t hi = __byte_perm(va[2][w], va[3][w], sel);
-                if constexpr (BITS == 4) {
-                    const uint32_t lo8 = lo >> 8, hi8 = hi >> 8;
-                    const int t = 4 * w + 2 * h;
+                for (int i = 0; i < 2; ++i) {
+                    const float ks = bf16_lo_to_f32(pa[u][i][2 * g]), kn = bf16_hi_to_f32(pa[u][i][2 * g]);
+                    const f2 ks2 = f2_of(ks, ks), kn2 = f2_of(kn, kn);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        mma_f16_16816(o[t][nt], lo & 0x000f000fu, lo & 0x00f000f0u, hi & 0x000f000fu,
-                                      hi & 0x00f000f0u, pb[t * NG / S][nt][0], pb[t * NG / S][nt][1]);
-                        mma_f16_16816(o[t + 1][nt], lo8 & 0x000f000fu, lo8 & 0x00f000f0u,
-                                      hi8 & 0x000f000fu, hi8 & 0x00f000f0u,
-                                      pb[(t + 1) * NG / S][nt][0], pb[(t + 1) * NG / S][nt][1]);
+                        const f2 base = g == 0 ? f2_mul(kn2, qsum[g][nt]) : f2_fma(kn2, qsum[g][nt], x[u][nt][i]);
+                        x[u][nt][i] = f2_fma(ks2, f2_of(acc[nt][2 * i], acc[nt][2 * i + 1]), base);
                     }
-                } else {
-                    const int t = 2 * w + h;
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        mma_f16_16816(o[t][nt], lo & 0x00ff00ffu, (lo >> 8) & 0x00ff00ffu,
-                                      hi & 0x00ff00ffu, (hi >> 8) & 0x00ff00ffu,
-                                      pb[t * NG / S][nt][0], pb[t * NG / S][nt][1]);
                 }
             }
+        }
+
+        // rows that do not count may hold anything, NaN parameters too
+        bool ok[UT][2];
+#pragma unroll
+        for (int u = 0; u < UT; ++u)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                ok[u][i] = !MASKED || ((rows[u] >> (quant_tile_row(gq) + 8 * i)) & 1u) != 0u;
+        auto hidden = [&](int u, int nt, int e) -> bool {
+            return MASKED && (!ok[u][e / 2] ||
+                              key0[u] + quant_tile_row(gq) + 8 * (e / 2) - tok[nt][e & 1] > last);
+        };
+        f2 vs[UT][NG][2], vn[UT][NG][2];      // scale and middle value of the rows at gq and at gq + 8
+#pragma unroll
+        for (int u = 0; u < UT; ++u)
+#pragma unroll
+            for (int g = 0; g < NG; ++g)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    float a = bf16_lo_to_f32(pa[u][i][2 * g + 1]);
+                    float b = __fmaf_rn(a, kMid, bf16_hi_to_f32(pa[u][i][2 * g + 1]));
+                    if (!ok[u][i]) a = b = 0.f;
+                    vs[u][g][i] = f2_of(a, a);
+                    vn[u][g][i] = f2_of(b, b);
+                }
+
+        // weights: p for the sums, p * f * vs for the product; all of them are non-negative, so a bound
+        // on their sum bounds each (a NaN fails the comparison and takes the careful path)
+        f2 pe[UT][NT][2], wt[UT][NG][NT][2], sum;
+        auto weights = [&]() {
+            sum = f2_of(0.f, 0.f);
+#pragma unroll
+            for (int u = 0; u < UT; ++u)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const f2 y = f2_fma(x[u][nt][i], cf[nt], nm[nt]);
+                        float a = fast_exp2(f2_get(y, 0)), b = fast_exp2(f2_get(y, 1));
+                        if (hidden(u, nt, 2 * i)) a = 0.f;
+                        if (hidden(u, nt, 2 * i + 1)) b = 0.f;
+                        pe[u][nt][i] = f2_of(a, b);
+                        sum = f2_add(sum, pe[u][nt][i]);
+                        const f2 pf = f2_mul(pe[u][nt][i], f[nt]);
+#pragma unroll
+                        for (int g = 0; g < NG; ++g) {
+                            f2 w = f2_mul(pf, vs[u][g][i]);
+                            // a key that the column does not see adds nothing, whatever its row holds
+                            if (MASKED)
+                                w = f2_of(hidden(u, nt, 2 * i) ? 0.f : f2_get(w, 0),
+                                          hidden(u, nt, 2 * i + 1) ? 0.f : f2_get(w, 1));
+                            wt[u][g][nt][i] = w;
+                            sum = f2_add(sum, w);
+                        }
+                    }
+        };
+        weights();
+        if (__any_sync(0xffffffffu, !(f2_get(sum, 0) + f2_get(sum, 1) <= 256.f))) {
+            float ls[UT][2];
+#pragma unroll
+            for (int u = 0; u < UT; ++u)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    float y = f2_get(vs[u][0][i], 0);
+#pragma unroll
+                    for (int g = 1; g < NG; ++g) y = fmaxf(y, f2_get(vs[u][g][i], 0));
+                    // a scale's exponent within [-64, 120]: 0 has none, and 2^(m - M) stays normal
+                    ls[u][i] = fminf(fmaxf(fast_log2(y), -64.f), 120.f);
+                }
+            raise(x, ls, hidden);
+            weights();
+        }
+        uint32_t pb[UT][NG][NT][2];
+#pragma unroll
+        for (int u = 0; u < UT; ++u)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                l[nt] = f2_add(l[nt], f2_add(pe[u][nt][0], pe[u][nt][1]));
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        if (MASKED) {
+                            const f2 y = f2_mul(pe[u][nt][i], vn[u][g][i]);
+                            z[g][nt] = f2_add(z[g][nt], f2_of(hidden(u, nt, 2 * i) ? 0.f : f2_get(y, 0),
+                                                              hidden(u, nt, 2 * i + 1) ? 0.f : f2_get(y, 1)));
+                        } else {
+                            z[g][nt] = f2_fma(pe[u][nt][i], vn[u][g][i], z[g][nt]);
+                        }
+                        pb[u][g][nt][i] = movmatrix_trans(
+                            pack_f16x2(f2_get(wt[u][g][nt][i], 0), f2_get(wt[u][g][nt][i], 1)));
+                    }
+                    mma_f16_16816(w0[g][nt], kMidLo, kMidHi, kMidLo, kMidHi, pb[u][g][nt][0],
+                                  pb[u][g][nt][1]);
+                }
+            }
+
+        // O^T += V^T P^T: pairs of keys for one element from the words of two rows
+#pragma unroll
+        for (int u = 0; u < UT; ++u) {
+            uint32_t va[4][VW];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                lds<VW>(stage + (i & 1 ? at[u].vb : at[u].va) + (i < 2 ? 0 : hk), va[i]);
+#pragma unroll
+            for (int w = 0; w < VW; ++w)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t sel = h ? 0x7632u : 0x5410u;
+                    const uint32_t lo = __byte_perm(va[0][w], va[1][w], sel);
+                    const uint32_t hi = __byte_perm(va[2][w], va[3][w], sel);
+                    if constexpr (BITS == 4) {
+                        const uint32_t lo8 = lo >> 8, hi8 = hi >> 8;
+                        const int t = 4 * w + 2 * h, ga = t * NG / S, gb = (t + 1) * NG / S;
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            mma_f16_16816(o[t][nt], lo & 0x000f000fu, lo & 0x00f000f0u,
+                                          hi & 0x000f000fu, hi & 0x00f000f0u, pb[u][ga][nt][0],
+                                          pb[u][ga][nt][1]);
+                            mma_f16_16816(o[t + 1][nt], lo8 & 0x000f000fu, lo8 & 0x00f000f0u,
+                                          hi8 & 0x000f000fu, hi8 & 0x00f000f0u, pb[u][gb][nt][0],
+                                          pb[u][gb][nt][1]);
+                        }
+                    } else {
+                        const int t = 2 * w + h, ga = t * NG / S;
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+                            mma_f16_16816(o[t][nt], lo & 0x00ff00ffu, (lo >> 8) & 0x00ff00ffu,
+                                          hi & 0x00ff00ffu, (hi >> 8) & 0x00ff00ffu, pb[u][ga][nt][0],
+                                          pb[u][ga][nt][1]);
+                    }
+                }
+        }
     }
 
     // Ends a segment: sums over the lanes, and o becomes sum p V relative to m (its final value but
     // for the division by l), so that m, l and o merge like any softmax state.
     __device__ __forceinline__ void settle() {
 #pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            auto over_lanes = [&](f2 v) {
+#pragma unroll
+                for (int off = 4; off < 32; off *= 2) v = f2_add(v, __shfl_xor_sync(0xffffffffu, v, off));
+                return v;
+            };
+            l[nt] = over_lanes(l[nt]);
+            const float back[2] = {fast_exp2(M[nt][0] + f2_get(nm[nt], 0)),
+                                   fast_exp2(M[nt][1] + f2_get(nm[nt], 1))};
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                const f2 zz = over_lanes(z[g][nt]);
+#pragma unroll
+                for (int i = g * S / NG; i < (g + 1) * S / NG; ++i)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        o[i][nt][e] = __fmaf_rn((o[i][nt][e] - w0[g][nt][e]) * kUnit, back[e], f2_get(zz, e));
+                        o[i][nt][e + 2] = __fmaf_rn((o[i][nt][e + 2] - w0[g][nt][e + 2]) * kUnitHi, back[e],
+                                                    f2_get(zz, e));
+                    }
+            }
+        }
+    }
+
+    // This warp's columns to its merge slot.
+    __device__ __forceinline__ void stash(const QuantSmem& sm, int warp) const {
+#pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-#pragma unroll
-                for (int off = 4; off < 32; off *= 2) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], off);
-                const float back = fast_exp2(M[nt][e] - m[nt][e]);
-#pragma unroll
-                for (int g = 0; g < NG; ++g) {
-#pragma unroll
-                    for (int off = 4; off < 32; off *= 2)
-                        z[g][nt][e] += __shfl_xor_sync(0xffffffffu, z[g][nt][e], off);
-#pragma unroll
-                    for (int i = g * S / NG; i < (g + 1) * S / NG; ++i) {
-                        o[i][nt][e] = __fmaf_rn(o[i][nt][e] * kUnit, back, z[g][nt][e]);
-                        o[i][nt][e + 2] = __fmaf_rn(o[i][nt][e + 2] * kUnitHi, back, z[g][nt][e]);
-                    }
+                const int c = warp * Gm::NC + nt * 8 + 2 * qd + e;
+                if (gq == 0) {
+                    sm.merge_m[c] = -f2_get(nm[nt], e);
+                    sm.merge_l[c] = f2_get(l[nt], e);
                 }
+                float* row = sm.merge_o + c * Gm::kMergeStride + 2 * gq;
+#pragma unroll
+                for (int i = 0; i < S; ++i)
+                    *reinterpret_cast<float2*>(row + 16 * i) = make_float2(o[i][nt][e], o[i][nt][e + 2]);
             }
-    }
-
-    // The columns of n-tile nt in merge slot `slot`.
-    __device__ __forceinline__ void stash(const QuantSmem& sm, int slot, int nt) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int c = slot * 8 + 2 * qd + e;
-            if (gq == 0) {
-                sm.merge_m[c] = m[nt][e];
-                sm.merge_l[c] = l[nt][e];
-            }
-            float* row = sm.merge_o + c * Gm::kMergeStride + 2 * gq;
-#pragma unroll
-            for (int i = 0; i < S; ++i)
-                *reinterpret_cast<float2*>(row + 16 * i) = make_float2(o[i][nt][e], o[i][nt][e + 2]);
-        }
-    }
-
-    // Merges merge slot `slot` into the columns of n-tile nt.
-    __device__ __forceinline__ void fold(const QuantSmem& sm, int slot, int nt) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int c = slot * 8 + 2 * qd + e;
-            const float m2 = sm.merge_m[c], top = fmaxf(m[nt][e], m2);
-            const float a = fast_exp2(m[nt][e] - top), b = fast_exp2(m2 - top);
-            m[nt][e] = top;
-            l[nt][e] = l[nt][e] * a + sm.merge_l[c] * b;
-            const float* row = sm.merge_o + c * Gm::kMergeStride + 2 * gq;
-#pragma unroll
-            for (int i = 0; i < S; ++i) {
-                const float2 y = *reinterpret_cast<const float2*>(row + 16 * i);
-                o[i][nt][e] = o[i][nt][e] * a + y.x * b;
-                o[i][nt][e + 2] = o[i][nt][e + 2] * a + y.y * b;
-            }
-        }
     }
 };
 
@@ -588,28 +763,41 @@ __device__ __forceinline__ void store_row4(__nv_bfloat16* p, float4 v) {
     *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
 }
 
-// Merges the nseg partial rows of a unit by log-sum-exp in segment order and stores its output.
+// Merges the nseg partial rows of a unit by log-sum-exp in segment order and stores its output.  The
+// loads of kAhead segments are in flight together, so a unit costs one trip to L2 per kAhead of them.
 template <class Gm>
 __device__ __forceinline__ void quant_merge_unit(const QuantParams& p, size_t row0, int first_seg,
                                                  int nseg) {
-    constexpr int D4 = Gm::D / 4;
+    constexpr int D4 = Gm::D / 4, kAhead = 8;
     const int SH = p.kh * p.cols;
     const float* lse = p.part_lse + static_cast<size_t>(first_seg) * SH;
     const float4* o = reinterpret_cast<const float4*>(p.part_o + static_cast<size_t>(first_seg) * SH * Gm::D);
     for (int i = threadIdx.x; i < SH * D4; i += Gm::kConsumers) {
         const int r = i / D4;
-        float top = -CUDART_INF_F;
-#pragma unroll 4
-        for (int k = 0; k < nseg; ++k) top = fmaxf(top, __ldcg(lse + static_cast<size_t>(k) * SH + r));
+        float top = -CUDART_INF_F, sum = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        float sum = 0.f;
-#pragma unroll 4
-        for (int k = 0; k < nseg; ++k) {
-            const float e = __ldcg(lse + static_cast<size_t>(k) * SH + r);
-            const float4 y = __ldcg(o + static_cast<size_t>(k) * SH * D4 + i);
-            const float w = e == -CUDART_INF_F ? 0.f : fast_exp2(e - top);   // an empty piece: zeros
-            sum += w;
-            acc = fma4(w, y, acc);
+        for (int k0 = 0; k0 < nseg; k0 += kAhead) {
+            float e[kAhead], best = top;
+            float4 y[kAhead];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const bool in = k0 + k < nseg;
+                e[k] = in ? __ldcg(lse + static_cast<size_t>(k0 + k) * SH + r) : -CUDART_INF_F;
+                y[k] = in ? __ldcg(o + static_cast<size_t>(k0 + k) * SH * D4 + i)
+                          : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) best = fmaxf(best, e[k]);
+            const float back = top == -CUDART_INF_F ? 0.f : fast_exp2(top - best);
+            top = best;
+            sum *= back;
+            acc = make_float4(acc.x * back, acc.y * back, acc.z * back, acc.w * back);
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const float w = e[k] == -CUDART_INF_F ? 0.f : fast_exp2(e[k] - top);   // an empty piece
+                sum += w;
+                acc = fma4(w, y[k], acc);
+            }
         }
         const float inv = sum == 0.f ? 0.f : 1.0f / sum;
         store_row4(p.out + row0 * Gm::D + static_cast<size_t>(i) * 4,
@@ -623,16 +811,18 @@ quant_attn_kernel(const QuantParams p) {
     using Gm = QuantGeometry<D, BITS, NG, NC>;
     extern __shared__ unsigned char smem_raw[];
     const QuantSmem sm = quant_carve<Gm>(smem_raw);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // (broadcast, so that the compiler knows it to be the same on every lane)
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < Gm::kStages; ++s) {
             mbar_init(sm.full + s, 1u);
-            mbar_init(sm.empty + s, Gm::W);
+            mbar_init(sm.empty + s, Gm::WG);
         }
         mbar_init(sm.group, Gm::kConsumers);
+        mbar_init(sm.stashed, Gm::W);
+        mbar_init(sm.combined, Gm::WG);
         *sm.abort = 0;
-        *sm.last_flag = 0;
         fence_mbarrier_init();
     }
     grid_dependency_wait();
@@ -678,33 +868,39 @@ quant_attn_kernel(const QuantParams p) {
     const int page_shift = 31 - __clz(P), pe_shift = 31 - __clz(pe);
     const int block = pe * Gm::ROW;              // bytes of one (page, head) in a stage
 
-    if (warp == Gm::W) {
+    if (warp >= Gm::W) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Gm::kCopyRegs));
         // ================================================================ copying warp
         const int npg = tok >> pe_shift;         // pages of a stage (<= 32)
         bool ok = true;
         int it = 0;
+        const int pw = warp - Gm::W;
+        if (pw >= Gm::kCopyWarps) return;
+        it = pw;
         QuantUnit U{};
-        U.nt = 0;
-        int nxt = -1;                            // this lane's page of the stage to come
+        int nxt = -1;                            // this lane's page of the warp's next stage
         auto fetch = [&](int t) {
             if (t >= t1) return;
-            if (t >= U.base + U.nt || U.nt == 0) U = quant_locate(p, sm, t);
+            if (U.nt == 0) U = quant_locate(p, sm, t);
+            while (t >= U.base + U.nt) U = quant_next(p, sm, U);
             const int slot = ((t - U.base) * tok >> page_shift) + lane;
             const bool in = lane < npg && slot < ((U.len + P - 1) >> page_shift);
             nxt = in ? __ldg(p.block_table + static_cast<size_t>(U.b) * p.max_pages + slot) : -1;
         };
-        fetch(t0);
-        for (int t = t0; t < t1; ++t, ++it) {
+        fetch(t0 + pw);
+        for (int t = t0 + pw; t < t1; t += Gm::kCopyWarps, it += Gm::kCopyWarps) {
             const int s = it % Gm::kStages;
             const uint32_t ph = (it / Gm::kStages) & 1;
             const int page = nxt, g = U.g, len = U.len, key0 = (t - U.base) * tok;
-            fetch(t + 1);                        // its latency passes while this stage's slot frees
-            if (!mbar_wait_warp(sm.empty + s, ph ^ 1u, sm.abort)) { ok = false; break; }
+            fetch(t + Gm::kCopyWarps);           // arrives while this stage's slot frees
+            if (!quant_wait<kNapCopy>(sm.empty + s, ph ^ 1u, sm.abort)) { ok = false; break; }
             const bool good = page >= 0 && page < p.num_pages;
             const unsigned pages = __ballot_sync(0xffffffffu, good);
             unsigned char* dst = sm.stages + s * Gm::kStageBytes;
             if (lane == 0) {
-                sm.stage_len[s] = min(tok, len - key0);
+                // plain: every row of the stage counts for every column, in pages of 16 rows or more
+                const bool plain = pe >= 16 && __popc(pages) == npg && key0 + tok <= len - (p.causal ? p.sq - 1 : 0);
+                sm.stage_len[s] = plain ? -1 : min(tok, len - key0);
                 sm.stage_pages[s] = pages;
                 mbar_arrive_expect_tx(sm.full + s, __popc(pages) * kh * block);
             }
@@ -739,7 +935,7 @@ quant_attn_kernel(const QuantParams p) {
             record_error(p.err, kErrWaitEmpty);
             if (lane == 0) {
                 // let every copy this warp issued land before the CTA can exit
-                for (int k = it - 1; k >= 0 && k >= it - Gm::kStages; --k)
+                for (int k = it - Gm::kCopyWarps; k >= 0 && k >= it - Gm::kStages; k -= Gm::kCopyWarps)
                     if (!mbar_wait(sm.full + (k % Gm::kStages), (k / Gm::kStages) & 1, nullptr, kWaitLimitNs)) {
                         record_error(p.err, kErrDrain);
                         break;
@@ -750,9 +946,11 @@ quant_attn_kernel(const QuantParams p) {
     }
 
     // ==================================================================== consumer warps
-    // Warp w: column slice w % CS, then KV head, then its share of that head's tiles.
-    const int cs = warp & ((1 << p.slices_shift) - 1);
-    const int wt = warp >> p.slices_shift, WT = Gm::W >> p.slices_shift;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Gm::kConsumerRegs));
+    // Warp w of group w / WG; inside the group: column slice, KV head, share of that head's tiles.
+    const int gw = warp % Gm::WG, grp = warp / Gm::WG;
+    const int cs = gw & ((1 << p.slices_shift) - 1);
+    const int wt = gw >> p.slices_shift, WT = Gm::WG >> p.slices_shift;
     const int head = wt & (kh - 1);
     const int kh_shift = 31 - __clz(kh);
     QuantWarp<Gm> cw;
@@ -774,83 +972,142 @@ quant_attn_kernel(const QuantParams p) {
     };
     QuantUnit U{};
     if (t0 < t1) {
+        uint2 raw[Gm::NT][D / 16];
         U = quant_locate(p, sm, t0);
-        cw.load_q(p, unit_row0(U) + head * p.cols);
+        cw.fetch_q(p, unit_row0(U) + head * p.cols, raw);
+        cw.set_q(p.scale_log2, raw);
     }
-    int it = 0;
+    // Tile i of a stage; the places of the warp's first UT tiles never change
+    auto place = [&](int i) {
+        const int r0 = (i >> kh_shift) * 16;               // first row of the tile
+        const int blk = ((r0 >> pe_shift) * kh + head) * block, rr = r0 & (pe - 1);
+        return cw.tile_at(blk + rr * Gm::RB, blk + (pe + rr) * Gm::RB, blk + 2 * pe * Gm::RB + rr * Gm::PB);
+    };
+    typename QuantWarp<Gm>::TileAt own[Gm::TPW][Gm::UT];
+#pragma unroll
+    for (int j = 0; j < Gm::TPW; ++j)
+#pragma unroll
+        for (int u = 0; u < Gm::UT; ++u) own[j][u] = place(wt + (j * Gm::UT + u) * WT);
+    int stage = grp;                    // the group takes every kGroups-th stage of the CTA's range
+    uint32_t phase = 0;
+    int pend_u[2], pend_first[2], pend_n[2], npend = 0;   // units of which this CTA stored a piece
+    size_t pend_row[2];
+    int skip = grp;                     // stages until the group's next one
+    uint32_t round = 0;                 // segments merged so far
     for (int t = t0; t < t1;) {
         const int tend = min(t1, U.base + U.nt);
         const bool whole = t == U.base && tend == U.base + U.nt;
         // rows a causal column may see: keys up to last + its token; without masking, every row
         const int last = p.causal ? U.len - p.sq : 0x7fffffff;
         cw.reset();
-        for (; t < tend; ++t, ++it) {
-            const int s = it % Gm::kStages;
-            const uint32_t ph = (it / Gm::kStages) & 1;
-            if (!mbar_wait_warp(sm.full + s, ph, sm.abort)) {
+        for (t += skip; t < tend; t += Gm::kGroups) {
+            if (!quant_wait<kNapConsumer>(sm.full + stage, phase, sm.abort)) {
                 *sm.abort = 1;
                 record_error(p.err, kErrWaitFull);
                 return;
             }
-            const int nvalid = static_cast<int>(sm.stage_len[s]);
-            const unsigned pages = sm.stage_pages[s];
-            const uint32_t base = smem_u32(sm.stages + s * Gm::kStageBytes);
-            const int key0 = (t - U.base) * tok;
-            for (int i = wt; i < Gm::kTiles; i += WT) {
-                const int r0 = (i >> kh_shift) * 16;       // first row of the tile
-                const int pg = r0 >> pe_shift;
-                const uint32_t blk = base + (pg * kh + head) * block;
-                const int rr = r0 & (pe - 1);
-                const uint32_t k = blk + rr * Gm::RB, v = k + pe * Gm::RB,
-                               par = blk + 2 * pe * Gm::RB + rr * Gm::PB;
-                const int n = nvalid - r0;
-                uint32_t rows = n >= 16 ? 0xffffu : n > 0 ? (1u << n) - 1u : 0u;
-                if (!((pages >> pg) & 1u)) rows &= pe >= 16 ? 0u : 0xff00u;
-                if (pe < 16 && !((pages >> (pg + 1)) & 1u)) rows &= 0x00ffu;
-                if (rows == 0u) continue;
-                if (rows == 0xffffu && key0 + r0 + 15 <= last)
-                    cw.template tile<false>(k, v, par, rows, 0, 0);
-                else
-                    cw.template tile<true>(k, v, par, rows, key0 + r0, last);
+            const int nvalid = sm.stage_len[stage];
+            const unsigned char* base = sm.stages + stage * Gm::kStageBytes;
+            auto take = [&](int i, const typename QuantWarp<Gm>::TileAt (&at)[Gm::UT]) {
+                uint32_t rows[Gm::UT];
+                int key[Gm::UT];
+#pragma unroll
+                for (int u = 0; u < Gm::UT; ++u) {
+                    rows[u] = 0xffffu;
+                    key[u] = 0;
+                }
+                if (nvalid < 0) {
+                    cw.template tiles<false>(base, at, rows, key, 0);
+                    return;
+                }
+                const unsigned pages = sm.stage_pages[stage];
+                uint32_t any = 0u;
+#pragma unroll
+                for (int u = 0; u < Gm::UT; ++u) {
+                    const int r0 = ((i + u * WT) >> kh_shift) * 16, pg = r0 >> pe_shift;
+                    const int n = nvalid - r0;
+                    key[u] = (t - U.base) * tok + r0;
+                    rows[u] = n >= 16 ? 0xffffu : n > 0 ? (1u << n) - 1u : 0u;
+                    if (!((pages >> pg) & 1u)) rows[u] &= pe >= 16 ? 0u : 0xff00u;
+                    if (pe < 16 && !((pages >> (pg + 1)) & 1u)) rows[u] &= 0x00ffu;
+                    any |= rows[u];
+                }
+                if (any != 0u) cw.template tiles<true>(base, at, rows, key, last);
+            };
+#pragma unroll
+            for (int j = 0; j < Gm::TPW; ++j) take(wt + j * Gm::UT * WT, own[j]);
+            // with the columns split over several warps, each has more tiles
+            for (int i = wt + Gm::TPW * Gm::UT * WT; i < Gm::kTiles; i += WT * Gm::UT) {
+                typename QuantWarp<Gm>::TileAt at[Gm::UT];
+#pragma unroll
+                for (int u = 0; u < Gm::UT; ++u) at[u] = place(i + u * WT);
+                take(i, at);
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(sm.empty + s);
-        }
-
-        // ---- end of the segment
-        cw.settle();
-        const int first_seg = tile_owner(U.base, N, C) + U.u;
-        const int nseg = tile_owner(U.base + U.nt - 1, N, C) + U.u - first_seg + 1;
-        const int seg = static_cast<int>(blockIdx.x) + U.u;
-        const int SH = kh * p.cols;
-        const size_t row0 = unit_row0(U);
-#pragma unroll
-        for (int nt = 0; nt < Gm::NT; ++nt) {
-            // warps past the eighth (same head and columns as warp - 8) are folded into those first
-            if (Gm::W == 16) {
-                if (warp >= 8) cw.stash(sm, warp - 8, nt);
-                if (!quant_sync(sm, gphase, p.err)) return;
-                if (warp < 8) cw.fold(sm, warp, nt);
-                __syncwarp();
+            if (lane == 0) mbar_arrive(sm.empty + stage);
+            stage += Gm::kGroups;
+            if (stage >= Gm::kStages) {
+                stage -= Gm::kStages;
+                phase ^= 1u;
             }
-            if (warp < 8) cw.stash(sm, warp, nt);
-            if (!quant_sync(sm, gphase, p.err)) return;
-            // rows of this round: (head, slice, column); their pieces lie in the slots of KS warps
+        }
+        skip = t - tend;
+        t = tend;
+
+        // ---- end of the segment: every warp leaves its columns in its merge slot and goes on to the
+        // next unit; the group that took the segment's last stage merges them when all are there (after
+        // the CTA's last segment every group takes part: nothing else is left to do).  With all warps
+        // waiting for one another here a segment cost 6000 to 7500 cycles of streaming.
+        const bool more = t < t1;
+        QuantUnit next = U;
+        if (more) next = quant_next(p, sm, U);
+        uint2 raw[Gm::NT][D / 16];          // the next unit's query rows, on their way during the merge
+        cw.settle();
+        if (round > 0 && !quant_wait<kNapGroup>(sm.combined, (round - 1) & 1, sm.abort)) {
+            *sm.abort = 1;
+            record_error(p.err, kErrWaitGroup);
+            return;
+        }
+        cw.stash(sm, warp);
+        if (more) cw.fetch_q(p, unit_row0(next) + head * p.cols, raw);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sm.stashed);
+        const size_t row0 = unit_row0(U);
+        int first_seg = 0, nseg = 1;
+        if (!whole) {
+            first_seg = tile_owner(U.base, N, C) + U.u;
+            nseg = tile_owner(U.base + U.nt - 1, N, C) + U.u - first_seg + 1;
+        }
+        if (!more || grp == (tend - 1 - t0) % Gm::kGroups) {
+            if (!quant_wait<kNapGroup>(sm.stashed, round & 1, sm.abort)) {
+                *sm.abort = 1;
+                record_error(p.err, kErrWaitGroup);
+                return;
+            }
+            // Output rows of the unit: (KV head, column); the pieces of one lie in the slots of the warps
+            // that shared the head's tiles and hold the column.
             constexpr int D4 = D / 4;
+            const int SH = kh * p.cols;
+            const size_t seg0 = static_cast<size_t>(static_cast<int>(blockIdx.x) + U.u) * SH;
             const int pieces_shift = p.slices_shift + kh_shift;
-            const int KS = 8 >> pieces_shift;
-            for (int i = threadIdx.x; i < (8 << pieces_shift) * D4; i += Gm::kConsumers) {
+            const int KS = (Gm::WG >> pieces_shift) * Gm::kGroups;
+            const int from = more ? gw * 32 + lane : static_cast<int>(threadIdx.x);
+            const int step = more ? Gm::WG * 32 : Gm::kConsumers;
+#pragma unroll 1
+            for (int i = from; i < SH * D4; i += step) {
                 const int d4 = i % D4, r = i / D4;
-                const int c = r & 7, vw = r >> 3;             // vw: head << slices_shift | slice
-                const int col = (vw & ((1 << p.slices_shift) - 1)) * NC + nt * 8 + c;
-                if (col >= p.cols) continue;
+                const int h = r / p.cols, col = r - h * p.cols;
+                // slot of piece k: warp (k << pieces_shift) | (h << slices_shift) | slice (a group's
+                // warps are a multiple of 1 << pieces_shift), column col % NC
+                const int slot0 = ((h << p.slices_shift) | (col / NC)) * NC + col % NC;
+                const int hop = NC << pieces_shift;
                 float top = kQuantUnset;
-                for (int k = 0; k < KS; ++k)
-                    top = fmaxf(top, sm.merge_m[((k << pieces_shift) + vw) * 8 + c]);
+                for (int k = 0; k < KS; ++k) top = fmaxf(top, sm.merge_m[slot0 + k * hop]);
                 float sum = 0.f;
                 float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
                 for (int k = 0; k < KS; ++k) {
-                    const int slot = ((k << pieces_shift) + vw) * 8 + c;
+                    const int slot = slot0 + k * hop;
                     const float w = fast_exp2(sm.merge_m[slot] - top);
                     sum += w * sm.merge_l[slot];
                     acc = fma4(w, *reinterpret_cast<const float4*>(
@@ -858,35 +1115,44 @@ quant_attn_kernel(const QuantParams p) {
                 }
                 const float inv = sum == 0.f ? 0.f : 1.0f / sum;   // no row at all: zeros
                 const float4 v = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-                const int ur = (vw >> p.slices_shift) * p.cols + col;
                 if (whole) {
-                    store_row4(p.out + (row0 + ur) * D + 4 * d4, v);
+                    store_row4(p.out + (row0 + r) * D + 4 * d4, v);
                 } else {
-                    const size_t pr = static_cast<size_t>(seg) * SH + ur;
-                    *reinterpret_cast<float4*>(p.part_o + pr * D + 4 * d4) = v;
-                    if (d4 == 0) p.part_lse[pr] = sum == 0.f ? -CUDART_INF_F : top + fast_log2(sum);
+                    *reinterpret_cast<float4*>(p.part_o + (seg0 + r) * D + 4 * d4) = v;
+                    if (d4 == 0) p.part_lse[seg0 + r] = sum == 0.f ? -CUDART_INF_F : top + fast_log2(sum);
                 }
             }
-            if (!quant_sync(sm, gphase, p.err)) return;
+            __syncwarp();
+            if (more && lane == 0) mbar_arrive(sm.combined);
         }
-        const QuantUnit done = U;
-        if (t < t1) {
-            U = quant_locate(p, sm, t);
-            cw.load_q(p, unit_row0(U) + head * p.cols);
-        }
-        if (!whole) {
-            // the barrier above orders every partial store before thread 0's release
-            if (threadIdx.x == 0) {
-                const unsigned prev = atomic_add_acq_rel_gpu(p.counters + done.u);
-                *sm.last_flag = prev == static_cast<unsigned>(nseg - 1) ? 1 : 0;
+        ++round;
+        if (!whole) {                       // at most twice: the range's first and last unit
+            const int k = npend++;
+            if (k == 0) {
+                pend_u[0] = U.u; pend_first[0] = first_seg; pend_n[0] = nseg; pend_row[0] = row0;
+            } else {
+                pend_u[1] = U.u; pend_first[1] = first_seg; pend_n[1] = nseg; pend_row[1] = row0;
             }
-            if (!quant_sync(sm, gphase, p.err)) return;
-            if (*sm.last_flag) {
-                quant_merge_unit<Gm>(p, row0, first_seg, nseg);
-                if (threadIdx.x == 0) p.counters[done.u] = 0u;
-            }
-            if (!quant_sync(sm, gphase, p.err)) return;
         }
+        if (more) cw.set_q(p.scale_log2, raw);
+        U = next;
+    }
+
+    // ---- count the stored pieces, once after the whole range, and merge the units they complete.
+    // The barrier orders every partial store before these releases.
+    if (npend == 0) return;
+    if (!quant_sync(sm, gphase, p.err)) return;
+    if (threadIdx.x < npend) {
+        const int k = threadIdx.x;
+        const unsigned prev = atomic_add_acq_rel_gpu(p.counters + (k ? pend_u[1] : pend_u[0]));
+        sm.last_flag[k] = prev == static_cast<unsigned>((k ? pend_n[1] : pend_n[0]) - 1) ? 1 : 0;
+    }
+    if (!quant_sync(sm, gphase, p.err)) return;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        if (k >= npend || !sm.last_flag[k]) continue;
+        quant_merge_unit<Gm>(p, pend_row[k], pend_first[k], pend_n[k]);
+        if (threadIdx.x == 0) p.counters[pend_u[k]] = 0u;
     }
 }
 
