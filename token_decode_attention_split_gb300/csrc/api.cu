@@ -672,9 +672,11 @@ extern "C" da_status decode_attn_paged_quant(
     if (sms <= 0) return DA_ERR_CUDA;
     QuantParams p{};
     p.cols = (Hq / Hkv) * Sq;
-    p.kh = quant_kv_heads(B, Hkv, p.cols, bits, sms);
-    const long long qunits = units / p.kh;
-    const WsLayout w = ws_layout(qunits, qunits + sms, p.kh * p.cols, D);
+    const int kh = quant_kv_heads(B, Hkv, p.cols, bits, sms);
+    while ((1 << p.kh_shift) < kh) ++p.kh_shift;
+    p.upb = Hkv / kh;
+    const long long qunits = units / kh;
+    const WsLayout w = ws_layout(qunits, qunits + sms, kh * p.cols, D);
     if (workspace_bytes < w.total) return DA_ERR_WORKSPACE_TOO_SMALL;
     p.q = static_cast<const __nv_bfloat16*>(q);
     p.out = static_cast<__nv_bfloat16*>(out);

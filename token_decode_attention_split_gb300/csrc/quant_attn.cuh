@@ -50,6 +50,7 @@
 #include <cuda_runtime.h>
 #include <math_constants.h>
 
+#include "f32x2.cuh"
 #include "launch.h"
 #include "ptx.cuh"
 #include "quant_format.h"
@@ -66,7 +67,7 @@ struct QuantParams {
     int B, Hq, Hkv;
     int cols;                    // query columns of one KV head: Hq / Hkv * sq
     int sq, causal;
-    int kh;                      // KV heads per unit, a power of two
+    int kh_shift, upb;           // log2 of the KV heads per unit, units per sequence: Hkv >> kh_shift
     int slices_shift;            // log2 of the warps that split a head's columns
     float scale_log2;
     unsigned* counters;          // one per unit, zero between calls
@@ -115,7 +116,7 @@ struct QuantGeometry {
     static constexpr int kStages =
         (kStagesFit > kMaxStages ? kMaxStages : kStagesFit) / kCopyWarps * kCopyWarps;
     static constexpr int kSmemBytes = 128 + kStages * kStageBytes + kFixedBytes;
-    static_assert(kStages >= kCopyWarps && kStages >= 2 && kStages % kCopyWarps == 0 && kStages % kGroups == 0 && kStageBytes % 128 == 0 && kTiles >= WG, "ring");
+    static_assert(kCopyWarps <= 3 && kStages >= kCopyWarps && kStages >= 2 && kStages % kCopyWarps == 0 && kStages % kGroups == 0 && kStageBytes % 128 == 0 && kTiles >= WG, "ring");
 };
 
 struct QuantSmem {
@@ -166,34 +167,47 @@ struct QuantUnit {
     int base;        // global index of the first stage
 };
 
+// The unit of stage t; a whole warp calls it.  The sequence is the last b with seq_prefix[b] * units per
+// sequence <= t: a ballot over every 32nd candidate, then one over the 32 in between.
 __device__ __forceinline__ QuantUnit quant_locate(const QuantParams& p, const QuantSmem& sm, int t) {
-    const int upb = p.Hkv / p.kh;
-    int lo = 0, hi = p.B - 1;            // largest b with seq_prefix[b] * upb <= t
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (sm.seq_prefix[mid] * upb <= t) lo = mid; else hi = mid - 1;
+    const int upb = p.upb, lane = threadIdx.x & 31;
+    int b = 0;
+    for (int hop = (p.B + 31) / 32 > 1 ? 32 : 1; hop > 0; hop = hop == 32 ? 1 : 0) {
+        const int c = b + lane * hop;
+        const bool at = c < p.B && sm.seq_prefix[c] * upb <= t;
+        b += (__popc(__ballot_sync(0xffffffffu, at)) - 1) * hop;
     }
     QuantUnit U;
-    U.b = lo;
-    U.nt = sm.seq_prefix[lo + 1] - sm.seq_prefix[lo];
-    const int r = t - sm.seq_prefix[lo] * upb;
+    U.b = b;
+    U.nt = sm.seq_prefix[b + 1] - sm.seq_prefix[b];
+    const int r = t - sm.seq_prefix[b] * upb;
     U.g = r / U.nt;
-    U.u = lo * upb + U.g;
-    U.len = sm.seq_len[lo];
-    U.base = sm.seq_prefix[lo] * upb + U.g * U.nt;
+    U.u = b * upb + U.g;
+    U.len = sm.seq_len[b];
+    U.base = sm.seq_prefix[b] * upb + U.g * U.nt;
     return U;
 }
+
+// The stages [0, N) over C CTAs: the first N % C take one more than the others.
+struct QuantSplit {
+    int q, r;
+    __device__ __forceinline__ int first(int c) const { return c * q + min(c, r); }
+    __device__ __forceinline__ int owner(int t) const {
+        const int longer = r * (q + 1);
+        return t < longer ? t / (q + 1) : r + (t - longer) / q;
+    }
+};
 
 // The unit after U (one exists): the next head group, or the next sequence with rows.
 __device__ __forceinline__ QuantUnit quant_next(const QuantParams& p, const QuantSmem& sm, QuantUnit U) {
     U.base += U.nt;
     ++U.u;
-    if (++U.g == p.Hkv / p.kh) {
+    if (++U.g == p.upb) {
         U.g = 0;
         do {
             ++U.b;
             U.nt = sm.seq_prefix[U.b + 1] - sm.seq_prefix[U.b];
-            if (U.nt == 0) U.u += p.Hkv / p.kh;
+            if (U.nt == 0) U.u += p.upb;
         } while (U.nt == 0);
         U.len = sm.seq_len[U.b];
     }
@@ -274,34 +288,6 @@ __device__ __forceinline__ void lds(const unsigned char* at, uint32_t (&r)[N]) {
     }
 }
 
-// Two fp32 numbers in a register pair and the packed arithmetic on them (one instruction for both).
-using f2 = unsigned long long;
-__device__ __forceinline__ f2 f2_of(float lo, float hi) {
-    f2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ float f2_get(f2 v, int i) {
-    float lo, hi;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-    return i ? hi : lo;
-}
-__device__ __forceinline__ f2 f2_fma(f2 a, f2 b, f2 c) {
-    f2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ f2 f2_mul(f2 a, f2 b) {
-    f2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ f2 f2_add(f2 a, f2 b) {
-    f2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-
 // Row of a 16-row tile (0..7; +8 for the second half) that stands at fragment row i: neighbouring
 // fragment rows lie in rows of unlike parity (the K loads of a quarter warp then cover all banks at
 // 64 bytes a row) and the rows 2 t, t = 0..3, are the first four (two of each parity for the V loads).
@@ -324,7 +310,7 @@ struct QuantWarp {
     static constexpr uint32_t kMidLo = kMid * 0x00010001u, kMidHi = (BITS == 4 ? 16 : 1) * kMidLo;
 
     int lane, gq, qd;                // fragment row, quad lane
-    int head, col0;                  // KV head of the unit, first query column
+    int col0;                        // first query column
     uint32_t qf[S][NT][2];           // Q^T fragments (fp16, scaled by a power of two per column)
     // pairs: columns 2 qd and 2 qd + 1 of an n-tile
     f2 qsum[NG][NT];                 // sum of a column's scaled elements per group, in code units
@@ -339,13 +325,8 @@ struct QuantWarp {
     int koff, voff[2], poff;         // lane offsets inside a tile: K row, V rows, parameters
     int half_k, half_p;              // from a row of the tile's first half to its second half
 
-    __device__ __forceinline__ void init(int lane_, int head_, int col0_, int sq, int half_k_,
-                                         int half_p_) {
-        lane = lane_;
-        gq = lane >> 2;
-        qd = lane & 3;
-        head = head_;
-        col0 = col0_;
+    // (lane, gq, qd and col0 are set)
+    __device__ __forceinline__ void init(int sq, int half_k_, int half_p_) {
         koff = quant_tile_row(gq) * Gm::RB + qd * (4 * KW);
         voff[0] = quant_tile_row(2 * qd) * Gm::RB + gq * (4 * VW);
         voff[1] = quant_tile_row(2 * qd + 1) * Gm::RB + gq * (4 * VW);
@@ -763,45 +744,66 @@ __device__ __forceinline__ void store_row4(__nv_bfloat16* p, float4 v) {
     *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
 }
 
-// Merges the nseg partial rows of a unit by log-sum-exp in segment order and stores its output.  The
-// loads of kAhead segments are in flight together, so a unit costs one trip to L2 per kAhead of them.
+// Merges the nseg partial rows of a unit by log-sum-exp in segment order and stores its output.  A
+// thread keeps the loads of kAhead segments of kRows rows in flight: a unit costs one trip to L2 per kAhead
+// segments and kRows * kConsumers / (D / 4) rows (the narrow kernels' units have few rows).
 template <class Gm>
 __device__ __forceinline__ void quant_merge_unit(const QuantParams& p, size_t row0, int first_seg,
                                                  int nseg) {
-    constexpr int D4 = Gm::D / 4, kAhead = 8;
-    const int SH = p.kh * p.cols;
+    constexpr int D4 = Gm::D / 4, kAhead = 8, kRows = Gm::NT, kHop = Gm::kConsumers / D4;
+    const int SH = p.cols << p.kh_shift, d4 = threadIdx.x % D4;
     const float* lse = p.part_lse + static_cast<size_t>(first_seg) * SH;
-    const float4* o = reinterpret_cast<const float4*>(p.part_o + static_cast<size_t>(first_seg) * SH * Gm::D);
-    for (int i = threadIdx.x; i < SH * D4; i += Gm::kConsumers) {
-        const int r = i / D4;
-        float top = -CUDART_INF_F, sum = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float4* o = reinterpret_cast<const float4*>(p.part_o + static_cast<size_t>(first_seg) * SH * Gm::D) + d4;
+#pragma unroll 1
+    for (int r0 = threadIdx.x / D4; r0 < SH; r0 += kRows * kHop) {
+        float top[kRows], sum[kRows];
+        float4 acc[kRows];
+#pragma unroll
+        for (int j = 0; j < kRows; ++j) {
+            top[j] = -CUDART_INF_F;
+            sum[j] = 0.f;
+            acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll 1
         for (int k0 = 0; k0 < nseg; k0 += kAhead) {
-            float e[kAhead], best = top;
-            float4 y[kAhead];
+            float e[kRows][kAhead];
+            float4 y[kRows][kAhead];
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k) {
-                const bool in = k0 + k < nseg;
-                e[k] = in ? __ldcg(lse + static_cast<size_t>(k0 + k) * SH + r) : -CUDART_INF_F;
-                y[k] = in ? __ldcg(o + static_cast<size_t>(k0 + k) * SH * D4 + i)
-                          : make_float4(0.f, 0.f, 0.f, 0.f);
-            }
+            for (int j = 0; j < kRows; ++j)
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k) best = fmaxf(best, e[k]);
-            const float back = top == -CUDART_INF_F ? 0.f : fast_exp2(top - best);
-            top = best;
-            sum *= back;
-            acc = make_float4(acc.x * back, acc.y * back, acc.z * back, acc.w * back);
+                for (int k = 0; k < kAhead; ++k) {
+                    const int r = r0 + j * kHop;
+                    const size_t at = static_cast<size_t>(k0 + k) * SH + r;
+                    const bool in = r < SH && k0 + k < nseg;
+                    e[j][k] = in ? __ldcg(lse + at) : -CUDART_INF_F;
+                    y[j][k] = in ? __ldcg(o + at * D4) : make_float4(0.f, 0.f, 0.f, 0.f);
+                }
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k) {
-                const float w = e[k] == -CUDART_INF_F ? 0.f : fast_exp2(e[k] - top);   // an empty piece
-                sum += w;
-                acc = fma4(w, y[k], acc);
+            for (int j = 0; j < kRows; ++j) {
+                float best = top[j];
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) best = fmaxf(best, e[j][k]);
+                const float back = top[j] == -CUDART_INF_F ? 0.f : fast_exp2(top[j] - best);
+                top[j] = best;
+                sum[j] *= back;
+                acc[j] = make_float4(acc[j].x * back, acc[j].y * back, acc[j].z * back, acc[j].w * back);
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) {
+                    // an empty piece weighs nothing
+                    const float w = e[j][k] == -CUDART_INF_F ? 0.f : fast_exp2(e[j][k] - best);
+                    sum[j] += w;
+                    acc[j] = fma4(w, y[j][k], acc[j]);
+                }
             }
         }
-        const float inv = sum == 0.f ? 0.f : 1.0f / sum;
-        store_row4(p.out + row0 * Gm::D + static_cast<size_t>(i) * 4,
-                   make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+#pragma unroll
+        for (int j = 0; j < kRows; ++j) {
+            const int r = r0 + j * kHop;
+            const float inv = sum[j] == 0.f ? 0.f : 1.0f / sum[j];
+            if (r < SH)
+                store_row4(p.out + (row0 + r) * Gm::D + 4 * d4,
+                           make_float4(acc[j].x * inv, acc[j].y * inv, acc[j].z * inv, acc[j].w * inv));
+        }
     }
 }
 
@@ -829,15 +831,15 @@ quant_attn_kernel(const QuantParams p) {
     allow_dependent_launch();
 
     // ---- schedule
-    const int kh = p.kh, P = p.page_size;
-    const int tok = Gm::kStageRows / kh;         // rows of one KV head in a stage
+    const int kh_shift = p.kh_shift, kh = 1 << kh_shift, P = p.page_size;
+    const int tok = Gm::kStageRows >> kh_shift;  // rows of one KV head in a stage
     {
         const int cap = p.max_pages * P;
         for (int b = threadIdx.x; b < p.B; b += Gm::kThreads) {
             const unsigned raw = __ldg(p.kv_lens + static_cast<size_t>(b) * p.kv_stride);
             const int len = raw > static_cast<unsigned>(cap) ? cap : static_cast<int>(raw);
             sm.seq_len[b] = len;
-            sm.seq_prefix[b + 1] = (len + tok - 1) / tok;
+            sm.seq_prefix[b + 1] = (len + tok - 1) >> (31 - __clz(tok));
         }
         __syncthreads();
         if (warp == 0) {
@@ -857,12 +859,15 @@ quant_attn_kernel(const QuantParams p) {
         }
     }
     __syncthreads();
-    const int N = sm.seq_prefix[p.B] * (p.Hkv / kh);
+    const int N = sm.seq_prefix[p.B] * p.upb;
     const int C = min(static_cast<int>(gridDim.x), N);
     int t0 = 0, t1 = 0;
+    QuantSplit split{1, 0};
     if (static_cast<int>(blockIdx.x) < C) {
-        t0 = static_cast<int>(static_cast<long long>(blockIdx.x) * N / C);
-        t1 = static_cast<int>(static_cast<long long>(blockIdx.x + 1) * N / C);
+        split.q = N / C;
+        split.r = N - C * split.q;
+        t0 = split.first(blockIdx.x);
+        t1 = split.first(blockIdx.x + 1);
     }
     const int pe = min(P, tok);                  // rows of one page in a stage
     const int page_shift = 31 - __clz(P), pe_shift = 31 - __clz(pe);
@@ -875,6 +880,15 @@ quant_attn_kernel(const QuantParams p) {
         bool ok = true;
         int it = 0;
         const int pw = warp - Gm::W;
+        if (pw == 3) {
+            // a warp without copies: zero output rows for sequences without rows
+            const size_t n = static_cast<size_t>(p.Hq) * p.sq * D / 8;
+            for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+                if (sm.seq_len[b] != 0) continue;
+                uint4* to = reinterpret_cast<uint4*>(p.out) + b * n;
+                for (size_t i = lane; i < n; i += 32) to[i] = make_uint4(0u, 0u, 0u, 0u);
+            }
+        }
         if (pw >= Gm::kCopyWarps) return;
         it = pw;
         QuantUnit U{};
@@ -952,31 +966,24 @@ quant_attn_kernel(const QuantParams p) {
     const int cs = gw & ((1 << p.slices_shift) - 1);
     const int wt = gw >> p.slices_shift, WT = Gm::WG >> p.slices_shift;
     const int head = wt & (kh - 1);
-    const int kh_shift = 31 - __clz(kh);
-    QuantWarp<Gm> cw;
-    // the second eight rows of a tile: next in the page, or on the next page (8-row pages)
-    cw.init(lane, head, cs * NC, p.sq, pe >= 16 ? 8 * Gm::RB : kh * block,
-            pe >= 16 ? 8 * Gm::PB : kh * block);
     uint32_t gphase = 0;
-
-    // sequences without rows: zero output rows
-    for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-        if (sm.seq_len[b] != 0) continue;
-        const size_t n = static_cast<size_t>(p.Hq) * p.sq * D;
-        for (size_t i = threadIdx.x; i < n; i += Gm::kConsumers)
-            p.out[b * n + i] = __float2bfloat16_rn(0.f);
-    }
 
     auto unit_row0 = [&](const QuantUnit& U) -> size_t {   // first q / out row of the unit
         return (static_cast<size_t>(U.b) * p.Hkv + U.g * kh) * p.cols;
     };
     QuantUnit U{};
+    QuantWarp<Gm> cw;
+    uint2 first[Gm::NT][D / 16];        // the first unit's query rows, on their way during the set-up
+    cw.lane = lane;
+    cw.gq = lane >> 2;
+    cw.qd = lane & 3;
+    cw.col0 = cs * NC;
     if (t0 < t1) {
-        uint2 raw[Gm::NT][D / 16];
         U = quant_locate(p, sm, t0);
-        cw.fetch_q(p, unit_row0(U) + head * p.cols, raw);
-        cw.set_q(p.scale_log2, raw);
+        cw.fetch_q(p, unit_row0(U) + head * p.cols, first);
     }
+    // the second eight rows of a tile: next in the page, or on the next page (8-row pages)
+    cw.init(p.sq, pe >= 16 ? 8 * Gm::RB : kh * block, pe >= 16 ? 8 * Gm::PB : kh * block);
     // Tile i of a stage; the places of the warp's first UT tiles never change
     auto place = [&](int i) {
         const int r0 = (i >> kh_shift) * 16;               // first row of the tile
@@ -988,6 +995,7 @@ quant_attn_kernel(const QuantParams p) {
     for (int j = 0; j < Gm::TPW; ++j)
 #pragma unroll
         for (int u = 0; u < Gm::UT; ++u) own[j][u] = place(wt + (j * Gm::UT + u) * WT);
+    if (t0 < t1) cw.set_q(p.scale_log2, first);
     int stage = grp;                    // the group takes every kGroups-th stage of the CTA's range
     uint32_t phase = 0;
     int pend_u[2], pend_first[2], pend_n[2], npend = 0;   // units of which this CTA stored a piece
@@ -1075,8 +1083,8 @@ quant_attn_kernel(const QuantParams p) {
         const size_t row0 = unit_row0(U);
         int first_seg = 0, nseg = 1;
         if (!whole) {
-            first_seg = tile_owner(U.base, N, C) + U.u;
-            nseg = tile_owner(U.base + U.nt - 1, N, C) + U.u - first_seg + 1;
+            first_seg = split.owner(U.base) + U.u;
+            nseg = split.owner(U.base + U.nt - 1) + U.u - first_seg + 1;
         }
         if (!more || grp == (tend - 1 - t0) % Gm::kGroups) {
             if (!quant_wait<kNapGroup>(sm.stashed, round & 1, sm.abort)) {
@@ -1091,23 +1099,23 @@ quant_attn_kernel(const QuantParams p) {
             const size_t seg0 = static_cast<size_t>(static_cast<int>(blockIdx.x) + U.u) * SH;
             const int pieces_shift = p.slices_shift + kh_shift;
             const int KS = (Gm::WG >> pieces_shift) * Gm::kGroups;
-            const int from = more ? gw * 32 + lane : static_cast<int>(threadIdx.x);
-            const int step = more ? Gm::WG * 32 : Gm::kConsumers;
-#pragma unroll 1
-            for (int i = from; i < SH * D4; i += step) {
-                const int d4 = i % D4, r = i / D4;
-                const int h = r / p.cols, col = r - h * p.cols;
+            const int tid = more ? gw * 32 + lane : static_cast<int>(threadIdx.x);
+            const int hop = (more ? Gm::WG * 32 : Gm::kConsumers) / D4;   // rows between a thread's own
+            const int d4 = tid % D4;
+            int h = 0, col = tid / D4;
+            while (col >= p.cols) { col -= p.cols; ++h; }
+#pragma unroll 2
+            for (int r = tid / D4; r < SH; r += hop) {
                 // slot of piece k: warp (k << pieces_shift) | (h << slices_shift) | slice (a group's
                 // warps are a multiple of 1 << pieces_shift), column col % NC
                 const int slot0 = ((h << p.slices_shift) | (col / NC)) * NC + col % NC;
-                const int hop = NC << pieces_shift;
+                const int step = NC << pieces_shift;
                 float top = kQuantUnset;
-                for (int k = 0; k < KS; ++k) top = fmaxf(top, sm.merge_m[slot0 + k * hop]);
+                for (int k = 0; k < KS; ++k) top = fmaxf(top, sm.merge_m[slot0 + k * step]);
                 float sum = 0.f;
                 float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
                 for (int k = 0; k < KS; ++k) {
-                    const int slot = slot0 + k * hop;
+                    const int slot = slot0 + k * step;
                     const float w = fast_exp2(sm.merge_m[slot] - top);
                     sum += w * sm.merge_l[slot];
                     acc = fma4(w, *reinterpret_cast<const float4*>(
@@ -1121,6 +1129,8 @@ quant_attn_kernel(const QuantParams p) {
                     *reinterpret_cast<float4*>(p.part_o + (seg0 + r) * D + 4 * d4) = v;
                     if (d4 == 0) p.part_lse[seg0 + r] = sum == 0.f ? -CUDART_INF_F : top + fast_log2(sum);
                 }
+                col += hop;
+                while (col >= p.cols) { col -= p.cols; ++h; }
             }
             __syncwarp();
             if (more && lane == 0) mbar_arrive(sm.combined);

@@ -30,12 +30,20 @@
 #include <cstdint>
 
 #include "decode_attn.h"
+#include "f32x2.cuh"
 #include "ptx.cuh"
 #include "quant_format.h"
 
 namespace {
 
+using da::f2;
+using da::f2_add;
+using da::f2_fma;
+using da::f2_get;
+using da::f2_of;
+
 constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
 
 struct CacheArgs {
     const __nv_bfloat16* k_new;   // append: rows [T] of [Hkv, D], k_stride / v_stride elements apart
@@ -48,6 +56,8 @@ struct CacheArgs {
     int64_t rows;                 // T
     int64_t num_slots;
     int Hkv;
+    int span;                     // KV heads that a warp takes of a row
+    int parts;                    // pieces of span heads in a row
     int page_shift, page_size;
     int page_bytes;
 };
@@ -55,6 +65,7 @@ struct CacheArgs {
 // Adding and subtracting 1.5 * 2^23 rounds a number below 2^22 to an integer (ties to even); the
 // sum's low bits are that integer.
 constexpr float kRound = 12582912.0f;
+constexpr uint32_t kRoundBits = 0x4b400000u;
 
 template <int D, int BITS>
 struct RowShape {
@@ -62,14 +73,15 @@ struct RowShape {
     static constexpr int kPer = 32 / BITS;                // codes per word
     static constexpr int S = D / 16;                      // 16-element slices
     static constexpr int kRowsPerWarp = 32 / kWords;
-    // element index of code i of stored word j
-    __device__ static constexpr int k_elem(int j, int i) {
-        const int pos = j * kPer + i, quad = pos / 4;
-        return 16 * (quad % S) + 4 * (quad / S) + pos % 4;
+    // Element of the first code of stored word j.  A word holds quads (K) or pairs (V) of consecutive
+    // 16-element slices of one lane part, so its i-th quad or pair lies 16 i elements further.
+    __device__ static int k_elem(int j) {
+        const int quad = j * (kPer / 4);
+        return 16 * (quad % S) + 4 * (quad / S);
     }
-    __device__ static constexpr int v_elem(int j, int i) {
-        const int pos = j * kPer + i, pair = pos / 2;
-        return 16 * (pair % S) + 2 * (pair / S) + pos % 2;
+    __device__ static int v_elem(int j) {
+        const int pair = j * (kPer / 2);
+        return 16 * (pair % S) + 2 * (pair / S);
     }
 };
 
@@ -81,11 +93,11 @@ __device__ __forceinline__ void load_elems(const __nv_bfloat16* row, int j,
     if (V) {
 #pragma unroll
         for (int i = 0; i < R::kPer / 2; ++i)
-            x[i] = __ldg(reinterpret_cast<const uint32_t*>(row + R::v_elem(j, 2 * i)));
+            x[i] = __ldg(reinterpret_cast<const uint32_t*>(row + R::v_elem(j) + 16 * i));
     } else {
 #pragma unroll
         for (int i = 0; i < R::kPer / 4; ++i) {
-            const uint2 y = __ldg(reinterpret_cast<const uint2*>(row + R::k_elem(j, 4 * i)));
+            const uint2 y = __ldg(reinterpret_cast<const uint2*>(row + R::k_elem(j) + 16 * i));
             x[2 * i] = y.x;
             x[2 * i + 1] = y.y;
         }
@@ -134,26 +146,33 @@ __device__ __forceinline__ uint32_t quantise_word(
         const float mx = __bfloat162float(__hmax_nan(hi.x, hi.y));
         const float range = mx - mn;
         const bool fine = range <= 3.4028234e38f;               // false for NaN and infinity
-        float s = __fdiv_rn(range, static_cast<float>((1 << BITS) - 1));
+        // range / (2^bits - 1), correctly rounded (Markstein: one residual correction with a correctly
+        // rounded reciprocal of the constant)
+        constexpr float kMax = static_cast<float>((1 << BITS) - 1), kInv = 1.0f / kMax;
+        const float s0 = range * kInv;
+        float s = __fmaf_rn(__fmaf_rn(-kMax, s0, range), kInv, s0);
         s = __uint_as_float((__float_as_uint(s) + 0xffffu) & 0xffff0000u);
         if (!fine || s < 1.17549435e-38f) s = 0.f;
         par[q] = fine ? (__float_as_uint(s) >> 16) | (__float_as_uint(mn) & 0xffff0000u)
                       : 0x7fc07fc0u;
         const float inv = s > 0.f ? __frcp_rz(s) : 0.f;
         const float base = fine ? mn : 0.f;
+        const f2 inv2 = f2_of(inv, inv), down = f2_of(-base, -base), minus = f2_of(-s, -s);
+        const f2 up = f2_of(kRound, kRound), back = f2_of(-kRound, -kRound);
+        uint32_t word = 0;     // sum of (kRoundBits + code) << position, modulo 2^32
+        uint32_t bias = 0;     // the kRoundBits in it
 #pragma unroll
-        for (int i = 0; i < kX; ++i)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const uint32_t w = x[q * kX + i];
-                const float v = e ? da::bf16_hi_to_f32(w) : da::bf16_lo_to_f32(w);
-                const float d = v - base;
-                const float k0 = __fadd_rn(__fmaf_rn(d, inv, kRound), -kRound);
-                const float res = __fmaf_rn(-k0, s, d);
-                const float c = __fadd_rn(__fmaf_rn(res, inv, k0), kRound);
-                const uint32_t code = __float_as_uint(c) & ((1u << BITS) - 1u);
-                packed |= (fine ? code : 0u) << (((q * kX + i) * 2 + e) * BITS);
-            }
+        for (int i = kX - 1; i >= 0; --i) {
+            const uint32_t w = x[q * kX + i];
+            const f2 d = f2_add(f2_of(da::bf16_lo_to_f32(w), da::bf16_hi_to_f32(w)), down);
+            const f2 k0 = f2_add(f2_fma(d, inv2, up), back);
+            const f2 res = f2_fma(k0, minus, d);
+            const f2 c = f2_add(f2_fma(res, inv2, k0), up);
+            word = (word * (1u << BITS) + __float_as_uint(f2_get(c, 1))) * (1u << BITS) +
+                   __float_as_uint(f2_get(c, 0));
+            bias = (bias * (1u << BITS) + kRoundBits) * (1u << BITS) + kRoundBits;
+        }
+        packed |= (fine ? word - bias : 0u) << (q * kX * 2 * BITS);
     }
     if (kQ == 1) par[1] = par[0];
     return packed;
@@ -174,117 +193,166 @@ struct WordPlace {
     }
 };
 
-// The page block and row of item (new row t, KV head h), or null where the slot says to skip it.
-__device__ __forceinline__ unsigned char* item_block(const CacheArgs& a, int64_t t, int h, int& row) {
-    const int64_t w = a.slots[t];
+// Block of KV head 0 of the page of slot w, and the row in it; null where the slot says to skip it.
+__device__ __forceinline__ unsigned char* slot_block(const CacheArgs& a, int64_t w, int& row) {
     if (w < 0 || w >= a.num_slots) return nullptr;
-    const int64_t page = w >> a.page_shift;
     row = static_cast<int>(w & (a.page_size - 1));
-    return a.pool + (page * a.Hkv + h) * a.page_bytes;
+    return a.pool + (w >> a.page_shift) * a.Hkv * a.page_bytes;
 }
 
+// Work of both kernels: a unit is `span` KV heads of one row, a warp takes one unit after another;
+// 32 / kWords heads go through the warp at a time, so many times, with the loads of all steps in flight
+// together.  The writer computes about 75 instructions per (row, KV head) and is fastest with two steps
+// and twice the CTAs that fit, so that new ones load while old ones compute (8192 rows of 8 heads, with
+// the rows read back: 22.0 us; four steps 24.5, one step 24.4, a grid of resident CTAs 25.1).  The reader
+// is bound by memory: four steps on a resident grid (131071 rows of 8 heads: 109.6 us, 6.28 TB/s; two
+// steps 116.5, twice the CTAs 115.2).
+constexpr int kCtasPerSm = 4;
+constexpr int kReadSteps = 4, kAppendSteps = 2;
+constexpr int kReadWaves = 1, kAppendWaves = 2;
+
 template <int D, int BITS, int GROUP>
-__global__ void __launch_bounds__(kThreads) quant_append_kernel(const CacheArgs a) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_append_kernel(const CacheArgs a) {
     using R = RowShape<D, BITS>;
     using PK = WordPlace<D, BITS, GROUP, false>;
     using PV = WordPlace<D, BITS, GROUP, true>;
     constexpr int RB = da::kQuantRowCodes(D, BITS), PB = da::kQuantRowParams(D, GROUP);
+    constexpr int X = R::kPer / 2;
     da::grid_dependency_wait();
     da::allow_dependent_launch();
     const int lane = threadIdx.x & 31;
     const int j = lane % R::kWords, sub = lane / R::kWords;
-    const int64_t items = a.rows * a.Hkv;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * (kThreads / 32) * R::kRowsPerWarp;
-    // the loop bound is the same on every lane of a warp (the shuffles need all of them)
-    for (int64_t it0 = (static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5)) *
-                       R::kRowsPerWarp;
-         it0 < items; it0 += step) {
-        const int64_t it = it0 + sub < items ? it0 + sub : items - 1;
-        const int64_t t = it / a.Hkv;
-        const int h = static_cast<int>(it - t * a.Hkv);
-        uint32_t xk[R::kPer / 2], xv[R::kPer / 2], pk[2], pv[2];
-        load_elems<D, BITS, false>(a.k_new + t * a.k_stride + h * D, j, xk);
-        load_elems<D, BITS, true>(a.v_new + t * a.v_stride + h * D, j, xv);
-        int row = 0;
-        unsigned char* block = item_block(a, t, h, row);
-        const uint32_t ck = quantise_word<D, BITS, GROUP, false>(xk, pk);
-        const uint32_t cv = quantise_word<D, BITS, GROUP, true>(xv, pv);
-        if (block == nullptr || it0 + sub >= items) continue;
-        *reinterpret_cast<uint32_t*>(block + row * RB + 4 * j) = ck;
-        *reinterpret_cast<uint32_t*>(block + (a.page_size + row) * RB + 4 * j) = cv;
-        unsigned char* par = block + 2 * a.page_size * RB + row * PB;
-        if (PK::stores(j)) *reinterpret_cast<uint32_t*>(par + 8 * PK::group(j)) = pk[0];
-        if (PV::stores(j)) {
+    const int64_t units = a.rows * a.parts;
+    // everything that decides the trip counts is the same on every lane of a warp (the shuffles need
+    // all of them)
+    for (int64_t u = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); u < units;
+         u += static_cast<int64_t>(gridDim.x) * kWarps) {
+        const int64_t t = a.parts == 1 ? u : u / a.parts;
+        const int h0 = static_cast<int>(u - t * a.parts) * a.span;
+        const int h1 = min(h0 + a.span, a.Hkv);
+        const int64_t slot = a.slots[t];
+        const __nv_bfloat16* kr = a.k_new + t * a.k_stride;
+        const __nv_bfloat16* vr = a.v_new + t * a.v_stride;
+        uint32_t xk[kAppendSteps][X], xv[kAppendSteps][X];
 #pragma unroll
-            for (int q = 0; q < PV::kQ; ++q)
-                *reinterpret_cast<uint32_t*>(par + 8 * (PV::group(j) + q) + 4) = pv[q];
+        for (int i = 0; i < kAppendSteps; ++i) {
+            const int h = min(h0 + i * R::kRowsPerWarp + sub, h1 - 1);
+            if (h0 + i * R::kRowsPerWarp >= h1) break;
+            load_elems<D, BITS, false>(kr + h * D, j, xk[i]);
+            load_elems<D, BITS, true>(vr + h * D, j, xv[i]);
+        }
+        int row = 0;
+        unsigned char* page = slot_block(a, slot, row);
+        if (page == nullptr) continue;
+#pragma unroll
+        for (int i = 0; i < kAppendSteps; ++i) {
+            const int h = h0 + i * R::kRowsPerWarp + sub;
+            if (h0 + i * R::kRowsPerWarp >= h1) break;
+            uint32_t pk[2], pv[2];
+            const uint32_t ck = quantise_word<D, BITS, GROUP, false>(xk[i], pk);
+            const uint32_t cv = quantise_word<D, BITS, GROUP, true>(xv[i], pv);
+            if (h >= h1) continue;
+            unsigned char* block = page + h * a.page_bytes;
+            *reinterpret_cast<uint32_t*>(block + row * RB + 4 * j) = ck;
+            *reinterpret_cast<uint32_t*>(block + (a.page_size + row) * RB + 4 * j) = cv;
+            unsigned char* par = block + 2 * a.page_size * RB + row * PB;
+            if (PK::stores(j)) *reinterpret_cast<uint32_t*>(par + 8 * PK::group(j)) = pk[0];
+            if (PV::stores(j)) {
+#pragma unroll
+                for (int q = 0; q < PV::kQ; ++q)
+                    *reinterpret_cast<uint32_t*>(par + 8 * (PV::group(j) + q) + 4) = pv[q];
+            }
         }
     }
 }
 
-// The bf16 values of stored word w; par(i): scale | min << 16 of the group of code i.
+// The bf16 values of stored word w; par: scale | min << 16 of the group (or two) of its codes.
 template <int D, int BITS, int GROUP, bool V>
-__device__ __forceinline__ void restore_word(uint32_t w, int j, const unsigned char* par,
+__device__ __forceinline__ void restore_word(uint32_t w, const uint32_t (&par)[2],
                                              uint32_t (&x)[RowShape<D, BITS>::kPer / 2]) {
     using R = RowShape<D, BITS>;
     using P = WordPlace<D, BITS, GROUP, V>;
     constexpr int kX = R::kPer / 2 / P::kQ;
+    const f2 back = f2_of(-8388608.f, -8388608.f);
+    // even and odd codes of a 4-bit word as bytes; a byte permute under the bits of 2^23 makes floats
+    const uint32_t even = BITS == 4 ? w & 0x0f0f0f0fu : w;
+    const uint32_t odd = BITS == 4 ? (w >> 4) & 0x0f0f0f0fu : w;
 #pragma unroll
     for (int q = 0; q < P::kQ; ++q) {
-        const uint32_t p = __ldg(reinterpret_cast<const uint32_t*>(par + 8 * (P::group(j) + q) +
-                                                                   (V ? 4 : 0)));
-        const float s = da::bf16_lo_to_f32(p), mn = da::bf16_hi_to_f32(p);
+        const float s = da::bf16_lo_to_f32(par[q]), mn = da::bf16_hi_to_f32(par[q]);
+        const f2 s2 = f2_of(s, s), mn2 = f2_of(mn, mn);
 #pragma unroll
         for (int i = 0; i < kX; ++i) {
-            float v[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const uint32_t code = (w >> (((q * kX + i) * 2 + e) * BITS)) & ((1u << BITS) - 1u);
-                const float c = __uint_as_float(0x4b400000u | code) - kRound;
-                v[e] = __fmaf_rn(s, c, mn);
-            }
-            x[q * kX + i] = da::pack_bf16x2(v[0], v[1]);
+            const int pair = q * kX + i;
+            const uint32_t lo = __byte_perm(even, 0x4b000000u, 0x7440 | (BITS == 4 ? pair : 2 * pair));
+            const uint32_t hi = __byte_perm(odd, 0x4b000000u, 0x7440 | (BITS == 4 ? pair : 2 * pair + 1));
+            const f2 c = f2_add(f2_of(__uint_as_float(lo), __uint_as_float(hi)), back);
+            const f2 v = f2_fma(s2, c, mn2);
+            x[pair] = da::pack_bf16x2(f2_get(v, 0), f2_get(v, 1));
         }
     }
 }
 
 template <int D, int BITS, int GROUP>
-__global__ void __launch_bounds__(kThreads) quant_read_kernel(const CacheArgs a) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_read_kernel(const CacheArgs a) {
     using R = RowShape<D, BITS>;
+    using PK = WordPlace<D, BITS, GROUP, false>;
+    using PV = WordPlace<D, BITS, GROUP, true>;
     constexpr int RB = da::kQuantRowCodes(D, BITS), PB = da::kQuantRowParams(D, GROUP);
+    constexpr int X = R::kPer / 2;
     da::grid_dependency_wait();
     da::allow_dependent_launch();
     const int lane = threadIdx.x & 31;
     const int j = lane % R::kWords, sub = lane / R::kWords;
-    const int64_t items = a.rows * a.Hkv;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * (kThreads / 32) * R::kRowsPerWarp;
-    for (int64_t it = (static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5)) *
-                          R::kRowsPerWarp + sub;
-         it < items; it += step) {
-        const int64_t t = it / a.Hkv;
-        const int h = static_cast<int>(it - t * a.Hkv);
+    const int64_t units = a.rows * a.parts, stride = static_cast<int64_t>(gridDim.x) * kWarps;
+    int64_t u = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+    if (u >= units) return;
+    int64_t t = a.parts == 1 ? u : u / a.parts;
+    int64_t slot = a.slots[t];
+    while (true) {
+        const int h0 = static_cast<int>(u - t * a.parts) * a.span;
+        const int h1 = min(h0 + a.span, a.Hkv);
         int row = 0;
-        const unsigned char* block = item_block(a, t, h, row);
-        uint32_t xk[R::kPer / 2], xv[R::kPer / 2];
-        if (block != nullptr) {
-            const uint32_t ck = __ldg(reinterpret_cast<const uint32_t*>(block + row * RB + 4 * j));
-            const uint32_t cv = __ldg(
-                reinterpret_cast<const uint32_t*>(block + (a.page_size + row) * RB + 4 * j));
+        const unsigned char* page = slot_block(a, slot, row);
+        uint32_t ck[kReadSteps], cv[kReadSteps], pk[kReadSteps][2], pv[kReadSteps][2];
+#pragma unroll
+        for (int i = 0; i < kReadSteps; ++i) {
+            ck[i] = cv[i] = pk[i][0] = pk[i][1] = pv[i][0] = pv[i][1] = 0u;   // a skipped row: zeros
+            const int h = h0 + i * R::kRowsPerWarp + sub;
+            if (page == nullptr || h >= h1) continue;
+            const unsigned char* block = page + h * a.page_bytes;
             const unsigned char* par = block + 2 * a.page_size * RB + row * PB;
-            restore_word<D, BITS, GROUP, false>(ck, j, par, xk);
-            restore_word<D, BITS, GROUP, true>(cv, j, par, xv);
-        } else {
+            ck[i] = __ldg(reinterpret_cast<const uint32_t*>(block + row * RB + 4 * j));
+            cv[i] = __ldg(reinterpret_cast<const uint32_t*>(block + (a.page_size + row) * RB + 4 * j));
+            pk[i][0] = __ldg(reinterpret_cast<const uint32_t*>(par + 8 * PK::group(j)));
 #pragma unroll
-            for (int i = 0; i < R::kPer / 2; ++i) xk[i] = xv[i] = 0u;
+            for (int q = 0; q < PV::kQ; ++q)
+                pv[i][q] = __ldg(reinterpret_cast<const uint32_t*>(par + 8 * (PV::group(j) + q) + 4));
         }
-        __nv_bfloat16* ko = a.k_out + it * D;
-        __nv_bfloat16* vo = a.v_out + it * D;
+        // the next unit's slot travels while this one is restored
+        const int64_t un = u + stride;
+        const int64_t tn = un < units ? (a.parts == 1 ? un : un / a.parts) : t;
+        slot = a.slots[tn];
+        __nv_bfloat16* ko = a.k_out + t * a.Hkv * D;
+        __nv_bfloat16* vo = a.v_out + t * a.Hkv * D;
 #pragma unroll
-        for (int i = 0; i < R::kPer / 4; ++i)
-            *reinterpret_cast<uint2*>(ko + R::k_elem(j, 4 * i)) = make_uint2(xk[2 * i], xk[2 * i + 1]);
+        for (int i = 0; i < kReadSteps; ++i) {
+            const int h = h0 + i * R::kRowsPerWarp + sub;
+            if (h >= h1) continue;
+            uint32_t xk[X], xv[X];
+            restore_word<D, BITS, GROUP, false>(ck[i], pk[i], xk);
+            restore_word<D, BITS, GROUP, true>(cv[i], pv[i], xv);
 #pragma unroll
-        for (int i = 0; i < R::kPer / 2; ++i)
-            *reinterpret_cast<uint32_t*>(vo + R::v_elem(j, 2 * i)) = xv[i];
+            for (int e = 0; e < R::kPer / 4; ++e)
+                *reinterpret_cast<uint2*>(ko + h * D + R::k_elem(j) + 16 * e) =
+                    make_uint2(xk[2 * e], xk[2 * e + 1]);
+#pragma unroll
+            for (int e = 0; e < X; ++e)
+                *reinterpret_cast<uint32_t*>(vo + h * D + R::v_elem(j) + 16 * e) = xv[e];
+        }
+        if (un >= units) break;
+        u = un;
+        t = tn;
     }
 }
 
@@ -320,7 +388,7 @@ da_status check(const void* pool, const int64_t* slots, int64_t T, int Hkv, int 
     return DA_OK;
 }
 
-da_status launch(Kernel kernel, CacheArgs& a, void* pool, const int64_t* slots, int64_t T, int Hkv,
+da_status launch(Kernel kernel, bool read, CacheArgs& a, void* pool, const int64_t* slots, int64_t T, int Hkv,
                  int D, int page_size, int64_t num_pages, int bits, int group, void* stream) {
     if (T == 0) return DA_OK;
     int dev = 0, sms = 0;
@@ -336,13 +404,20 @@ da_status launch(Kernel kernel, CacheArgs& a, void* pool, const int64_t* slots, 
     a.page_shift = 0;
     while ((1 << a.page_shift) < page_size) ++a.page_shift;
     a.page_bytes = page_size * da::kQuantRowBytes(D, bits, group);
-    const int64_t per_block = kThreads / (D * bits / 32);
-    const int64_t want = (T * Hkv + per_block - 1) / per_block;
+    const int steps = read ? kReadSteps : kAppendSteps;
+    // Heads of a unit: all that the kernel's steps cover, unless that leaves SMs without a warp of
+    // their own (few rows: the heads of a row then go to more warps).
+    const int at_once = 32 / (D * bits / 32);
+    a.span = steps * at_once;
+    if (T * ((Hkv + a.span - 1) / a.span) < sms) a.span = at_once;
+    a.parts = (Hkv + a.span - 1) / a.span;
+    const int64_t want = (T * a.parts + kWarps - 1) / kWarps;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(want < 8LL * sms ? want : 8LL * sms));
+        const int64_t most = static_cast<int64_t>(kCtasPerSm) * (read ? kReadWaves : kAppendWaves) * sms;
+    cfg.gridDim = dim3(static_cast<unsigned>(want < most ? want : most));
     cfg.blockDim = dim3(kThreads);
     cfg.stream = static_cast<cudaStream_t>(stream);
     cfg.attrs = attr;
@@ -376,7 +451,7 @@ extern "C" da_status decode_attn_append_paged_quant(
     a.v_new = static_cast<const __nv_bfloat16*>(v_new);
     a.k_stride = k_row_stride;
     a.v_stride = v_row_stride;
-    return launch(pick<false>(D, bits, group), a, pool, slot_mapping, T, Hkv, D, page_size,
+    return launch(pick<false>(D, bits, group), false, a, pool, slot_mapping, T, Hkv, D, page_size,
                   num_pages, bits, group, stream);
 }
 
@@ -390,6 +465,6 @@ extern "C" da_status decode_attn_read_paged_quant(const void* pool, const int64_
     CacheArgs a{};
     a.k_out = static_cast<__nv_bfloat16*>(k_out);
     a.v_out = static_cast<__nv_bfloat16*>(v_out);
-    return launch(pick<true>(D, bits, group), a, const_cast<void*>(pool), slot_mapping, T, Hkv, D,
+    return launch(pick<true>(D, bits, group), true, a, const_cast<void*>(pool), slot_mapping, T, Hkv, D,
                   page_size, num_pages, bits, group, stream);
 }
