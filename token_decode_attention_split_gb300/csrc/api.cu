@@ -191,16 +191,17 @@ constexpr long long kShortUnitTiles = 8;
 
 // Quantised paged units: warps that split a KV head's `cols` query columns (log2), and the KV heads
 // per unit: the most (a power of two dividing Hkv) that leave each head a warp of every group of
-// consumer warps and still give units for 80% of the SMs, one otherwise.  More heads per unit make
-// fewer and larger copies and fewer segment ends (64 ragged sequences of 8 KV heads: 181 us with four
-// heads a unit, 187 with two, 199 with one); fewer spread the merges of split units over more CTAs
-// (16 sequences of 4096 rows: 22.0 us with one, 22.9 with two, 25.7 with four).
+// consumer warps and still give units for 80% of the SMs (40% with more than 8 columns), one
+// otherwise.  More heads per unit make fewer and larger copies and fewer segment ends (64 ragged
+// sequences of 8 KV heads: 181 us with four heads a unit, 187 with two, 199 with one); fewer spread the
+// merges of split units over more CTAs (16 sequences of 4096 rows: 22.0 us with one, 22.9 with two, 25.7
+// with four).  Segment ends of wide units cost more (16 columns, 16 ragged sequences: 56 us with two, 65 with one).
 int quant_slices_shift(int cols) { return cols <= 16 ? 0 : cols <= 32 ? 1 : 2; }
 int quant_kv_heads(int B, int Hkv, int cols, int bits, int sms) {
     const int warps = bits == 4 && cols <= 8 ? 4 : 8;
     int kh = 1;
     while (Hkv % (2 * kh) == 0 && (2 * kh << quant_slices_shift(cols)) <= warps &&
-           5ll * B * (Hkv / (2 * kh)) >= 4ll * sms)
+           5ll * B * (Hkv / (2 * kh)) >= (cols > 8 ? 2ll : 4ll) * sms)
         kh *= 2;
     return kh;
 }

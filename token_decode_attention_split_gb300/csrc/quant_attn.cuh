@@ -374,54 +374,55 @@ struct QuantWarp {
         }
     }
     __device__ __forceinline__ void set_q(float scale_log2, const uint2 (&raws)[NT][S]) {
+        auto larger = [](uint32_t a, uint32_t b) {   // per half: the larger magnitude
+            const __nv_bfloat162 m = __hmax2(*reinterpret_cast<__nv_bfloat162*>(&a),
+                                             __habs2(*reinterpret_cast<__nv_bfloat162*>(&b)));
+            return *reinterpret_cast<const uint32_t*>(&m);
+        };
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const uint2(&raw)[S] = raws[nt];
             uint32_t top = 0;
 #pragma unroll
-            for (int s = 0; s < S; ++s) {
-                top = max(top, max((raw[s].x << 16) & 0x7fffffffu, raw[s].x & 0x7fff0000u));
-                top = max(top, max((raw[s].y << 16) & 0x7fffffffu, raw[s].y & 0x7fff0000u));
-            }
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            // the largest element goes to [2^14, 2^15)
-            const int ex = min(max(static_cast<int>(top >> 23), 27), 254);
+            for (int s = 0; s < S; ++s) top = larger(larger(top, raw[s].x), raw[s].y);
+            top = larger(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = larger(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            top = max(top >> 16, top & 0xffffu);
+            // the largest element goes to [2^14, 2^15) (an infinity stays one, a NaN spoils its row)
+            const int ex = min(max(static_cast<int>(top >> 7), 27), 254);
             const float up = __int_as_float((268 - ex) << 23);
             const float down = __int_as_float((ex - 14) << 23);
-            float gs[NG];
-#pragma unroll
-            for (int g = 0; g < NG; ++g) gs[g] = 0.f;
-            float v[S][4];
+            // 4 bits: a word holds two slices; its masked pairs are codes i and i + 4, at 2^-24 for even
+            // i and at 2^-20 for odd i, whose Q elements are therefore scaled by 2^-4 more
+            constexpr float kOdd = BITS == 4 ? 0.0625f : 1.0f;
+            const f2 up2 = f2_of(up, up * kOdd);
+            f2 v[S][2], gs[NG];
 #pragma unroll
             for (int s = 0; s < S; ++s) {
-                v[s][0] = bf16_lo_to_f32(raw[s].x) * up;
-                v[s][1] = bf16_hi_to_f32(raw[s].x) * up;
-                v[s][2] = bf16_lo_to_f32(raw[s].y) * up;
-                v[s][3] = bf16_hi_to_f32(raw[s].y) * up;
-                gs[s * NG / S] += (v[s][0] + v[s][1]) + (v[s][2] + v[s][3]);
+                v[s][0] = f2_mul(f2_of(bf16_lo_to_f32(raw[s].x), bf16_hi_to_f32(raw[s].x)), up2);
+                v[s][1] = f2_mul(f2_of(bf16_lo_to_f32(raw[s].y), bf16_hi_to_f32(raw[s].y)), up2);
+                const f2 both = f2_add(v[s][0], v[s][1]);
+                gs[s * NG / S] = s % (S / NG) == 0 ? both : f2_add(gs[s * NG / S], both);
             }
             if (BITS == 8) {
 #pragma unroll
-                for (int s = 0; s < S; ++s) {
-                    qf[s][nt][0] = pack_f16x2(v[s][0], v[s][1]);
-                    qf[s][nt][1] = pack_f16x2(v[s][2], v[s][3]);
-                }
-            } else {
-                // a word holds two slices; its masked pairs are codes i and i + 4, at 2^-24 for
-                // i = 0, 2 and at 2^-20 for i = 1, 3
+                for (int s = 0; s < S; ++s)
 #pragma unroll
-                for (int w = 0; w < S / 2; ++w) {
-                    qf[2 * w][nt][0] = pack_f16x2(v[2 * w][0], v[2 * w + 1][0]);
-                    qf[2 * w][nt][1] = pack_f16x2(v[2 * w][2], v[2 * w + 1][2]);
-                    qf[2 * w + 1][nt][0] = pack_f16x2(v[2 * w][1] * 0.0625f, v[2 * w + 1][1] * 0.0625f);
-                    qf[2 * w + 1][nt][1] = pack_f16x2(v[2 * w][3] * 0.0625f, v[2 * w + 1][3] * 0.0625f);
-                }
+                    for (int i = 0; i < 2; ++i)
+                        qf[s][nt][i] = pack_f16x2(f2_get(v[s][i], 0), f2_get(v[s][i], 1));
+            } else {
+#pragma unroll
+                for (int w = 0; w < S / 2; ++w)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            qf[2 * w + h][nt][i] = pack_f16x2(f2_get(v[2 * w][i], h), f2_get(v[2 * w + 1][i], h));
             }
             // to the score fragment's columns 2 qd, 2 qd + 1 (held here by the quads of those rows)
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
-                float x = gs[g];
+                float x = __fmaf_rn(f2_get(gs[g], 1), 1.f / kOdd, f2_get(gs[g], 0));
                 x += __shfl_xor_sync(0xffffffffu, x, 1);
                 x += __shfl_xor_sync(0xffffffffu, x, 2);
                 x *= 1.f / kUnit;
@@ -1110,13 +1111,19 @@ quant_attn_kernel(const QuantParams p) {
                 // warps are a multiple of 1 << pieces_shift), column col % NC
                 const int slot0 = ((h << p.slices_shift) | (col / NC)) * NC + col % NC;
                 const int step = NC << pieces_shift;
-                float top = kQuantUnset;
-                for (int k = 0; k < KS; ++k) top = fmaxf(top, sm.merge_m[slot0 + k * step]);
+                float pm[Gm::W], top = kQuantUnset;
+#pragma unroll
+                for (int k = 0; k < Gm::W; ++k) {
+                    pm[k] = k < KS ? sm.merge_m[slot0 + k * step] : kQuantUnset;
+                    top = fmaxf(top, pm[k]);
+                }
                 float sum = 0.f;
                 float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-                for (int k = 0; k < KS; ++k) {
+#pragma unroll
+                for (int k = 0; k < Gm::W; ++k) {
+                    if (k >= KS) break;
                     const int slot = slot0 + k * step;
-                    const float w = fast_exp2(sm.merge_m[slot] - top);
+                    const float w = fast_exp2(pm[k] - top);
                     sum += w * sm.merge_l[slot];
                     acc = fma4(w, *reinterpret_cast<const float4*>(
                                       sm.merge_o + slot * Gm::kMergeStride + 4 * d4), acc);
