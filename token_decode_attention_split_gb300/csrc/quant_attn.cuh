@@ -23,8 +23,9 @@
 // bf16 rounding is 0.0017).
 //
 // Work.  A unit is one sequence and kh adjacent KV heads; a stage is 128 or 256 rows, split evenly
-// over those heads.  The stages of all units are laid end to end and CTA c of a persistent grid
-// (one per SM) takes an equal contiguous range; its piece of a unit is a segment.  A page of kh
+// over those heads.  The stages of all units are laid end to end, each unit followed by unit_pad empty
+// places for the time that its end takes, and CTA c of a persistent grid (one per SM) takes an equal
+// contiguous range of places; its piece of a unit is a segment.  A page of kh
 // heads is contiguous (codes and parameters), so a stage is a few bulk copies.  The warps of a copying
 // warpgroup fill a ring of stages; consumer warps each take 16-row tiles of one KV head: S^T = K Q^T
 // and O^T += V^T P^T on mma.m16n8k16 with the keys (then the elements of V) on M and the query columns
@@ -68,6 +69,7 @@ struct QuantParams {
     int cols;                    // query columns of one KV head: Hq / Hkv * sq
     int sq, causal;
     int kh_shift, upb;           // log2 of the KV heads per unit, units per sequence: Hkv >> kh_shift
+    int unit_pad;                // empty places after a unit's stages
     int slices_shift;            // log2 of the warps that split a head's columns
     float scale_log2;
     unsigned* counters;          // one per unit, zero between calls
@@ -133,7 +135,7 @@ struct QuantSmem {
     unsigned* stage_pages;   // bit i: page i of the stage was copied
     volatile int* abort;
     int* last_flag;      // [2]
-    int* seq_prefix;     // [B + 1] exclusive prefix of the sequences' stages
+    int* seq_prefix;     // [B + 1] exclusive prefix of the sequences' places (of one unit each)
     int* seq_len;        // [B]
 };
 
@@ -164,7 +166,7 @@ __device__ __forceinline__ QuantSmem quant_carve(unsigned char* raw) {
 struct QuantUnit {
     int b, g, u;     // sequence, group of kh KV heads, unit index
     int len, nt;     // live rows, stages
-    int base;        // global index of the first stage
+    int base;        // place of the first stage
 };
 
 // The unit of stage t; a whole warp calls it.  The sequence is the last b with seq_prefix[b] * units per
@@ -179,12 +181,13 @@ __device__ __forceinline__ QuantUnit quant_locate(const QuantParams& p, const Qu
     }
     QuantUnit U;
     U.b = b;
-    U.nt = sm.seq_prefix[b + 1] - sm.seq_prefix[b];
+    const int places = sm.seq_prefix[b + 1] - sm.seq_prefix[b];
+    U.nt = places - p.unit_pad;
     const int r = t - sm.seq_prefix[b] * upb;
-    U.g = r / U.nt;
+    U.g = r / places;
     U.u = b * upb + U.g;
     U.len = sm.seq_len[b];
-    U.base = sm.seq_prefix[b] * upb + U.g * U.nt;
+    U.base = sm.seq_prefix[b] * upb + U.g * places;
     return U;
 }
 
@@ -198,9 +201,15 @@ struct QuantSplit {
     }
 };
 
-// The unit after U (one exists): the next head group, or the next sequence with rows.
-__device__ __forceinline__ QuantUnit quant_next(const QuantParams& p, const QuantSmem& sm, QuantUnit U) {
-    U.base += U.nt;
+// The unit after U: the next head group, or the next sequence with rows; past the last unit, one that
+// begins at `end`.
+__device__ __forceinline__ QuantUnit quant_next(const QuantParams& p, const QuantSmem& sm, QuantUnit U,
+                                                int end) {
+    U.base += U.nt + p.unit_pad;
+    if (U.base >= end) {
+        U.base = end;
+        return U;
+    }
     ++U.u;
     if (++U.g == p.upb) {
         U.g = 0;
@@ -209,6 +218,7 @@ __device__ __forceinline__ QuantUnit quant_next(const QuantParams& p, const Quan
             U.nt = sm.seq_prefix[U.b + 1] - sm.seq_prefix[U.b];
             if (U.nt == 0) U.u += p.upb;
         } while (U.nt == 0);
+        U.nt -= p.unit_pad;
         U.len = sm.seq_len[U.b];
     }
     return U;
@@ -840,7 +850,7 @@ quant_attn_kernel(const QuantParams p) {
             const unsigned raw = __ldg(p.kv_lens + static_cast<size_t>(b) * p.kv_stride);
             const int len = raw > static_cast<unsigned>(cap) ? cap : static_cast<int>(raw);
             sm.seq_len[b] = len;
-            sm.seq_prefix[b + 1] = (len + tok - 1) >> (31 - __clz(tok));
+            sm.seq_prefix[b + 1] = len == 0 ? 0 : ((len + tok - 1) >> (31 - __clz(tok))) + p.unit_pad;
         }
         __syncthreads();
         if (warp == 0) {
@@ -894,20 +904,41 @@ quant_attn_kernel(const QuantParams p) {
         it = pw;
         QuantUnit U{};
         int nxt = -1;                            // this lane's page of the warp's next stage
-        auto fetch = [&](int t) {
+        int t = t0;
+        if (t < t1) {
+            U = quant_locate(p, sm, t);
+            if (t >= U.base + U.nt) {            // a range may begin behind a unit's last stage
+                U = quant_next(p, sm, U, t1);
+                t = U.base;
+            }
+        }
+        // n stages further: t1 when the range has no more
+        auto advance = [&](int n) {
+            while (t < t1) {
+                const int here = min(t1, U.base + U.nt) - t;
+                if (n < here) {
+                    t += n;
+                    return;
+                }
+                n -= here;
+                U = quant_next(p, sm, U, t1);
+                t = U.base;
+            }
+        };
+        auto fetch = [&]() {
             if (t >= t1) return;
-            if (U.nt == 0) U = quant_locate(p, sm, t);
-            while (t >= U.base + U.nt) U = quant_next(p, sm, U);
             const int slot = ((t - U.base) * tok >> page_shift) + lane;
             const bool in = lane < npg && slot < ((U.len + P - 1) >> page_shift);
             nxt = in ? __ldg(p.block_table + static_cast<size_t>(U.b) * p.max_pages + slot) : -1;
         };
-        fetch(t0 + pw);
-        for (int t = t0 + pw; t < t1; t += Gm::kCopyWarps, it += Gm::kCopyWarps) {
+        advance(pw);
+        fetch();
+        for (; t < t1; it += Gm::kCopyWarps) {
             const int s = it % Gm::kStages;
             const uint32_t ph = (it / Gm::kStages) & 1;
             const int page = nxt, g = U.g, len = U.len, key0 = (t - U.base) * tok;
-            fetch(t + Gm::kCopyWarps);           // arrives while this stage's slot frees
+            advance(Gm::kCopyWarps);
+            fetch();                             // arrives while this stage's slot frees
             if (!quant_wait<kNapCopy>(sm.empty + s, ph ^ 1u, sm.abort)) { ok = false; break; }
             const bool good = page >= 0 && page < p.num_pages;
             const unsigned pages = __ballot_sync(0xffffffffu, good);
@@ -979,8 +1010,15 @@ quant_attn_kernel(const QuantParams p) {
     cw.gq = lane >> 2;
     cw.qd = lane & 3;
     cw.col0 = cs * NC;
-    if (t0 < t1) {
-        U = quant_locate(p, sm, t0);
+    int t = t0;
+    if (t < t1) {
+        U = quant_locate(p, sm, t);
+        if (t >= U.base + U.nt) {
+            U = quant_next(p, sm, U, t1);
+            t = U.base;
+        }
+    }
+    if (t < t1) {
         cw.fetch_q(p, unit_row0(U) + head * p.cols, first);
     }
     // the second eight rows of a tile: next in the page, or on the next page (8-row pages)
@@ -996,15 +1034,17 @@ quant_attn_kernel(const QuantParams p) {
     for (int j = 0; j < Gm::TPW; ++j)
 #pragma unroll
         for (int u = 0; u < Gm::UT; ++u) own[j][u] = place(wt + (j * Gm::UT + u) * WT);
-    if (t0 < t1) cw.set_q(p.scale_log2, first);
+    if (t < t1) cw.set_q(p.scale_log2, first);
     int stage = grp;                    // the group takes every kGroups-th stage of the CTA's range
     uint32_t phase = 0;
     int pend_u[2], pend_first[2], pend_n[2], npend = 0;   // units of which this CTA stored a piece
     size_t pend_row[2];
     int skip = grp;                     // stages until the group's next one
     uint32_t round = 0;                 // segments merged so far
-    for (int t = t0; t < t1;) {
+    int done = 0;                       // stages of the range in earlier segments
+    while (t < t1) {
         const int tend = min(t1, U.base + U.nt);
+        done += tend - t;
         const bool whole = t == U.base && tend == U.base + U.nt;
         // rows a causal column may see: keys up to last + its token; without masking, every row
         const int last = p.causal ? U.len - p.sq : 0x7fffffff;
@@ -1067,9 +1107,9 @@ quant_attn_kernel(const QuantParams p) {
         // next unit; the group that took the segment's last stage merges them when all are there (after
         // the CTA's last segment every group takes part: nothing else is left to do).  With all warps
         // waiting for one another here a segment cost 6000 to 7500 cycles of streaming.
+        const QuantUnit next = quant_next(p, sm, U, t1);
+        t = next.base;
         const bool more = t < t1;
-        QuantUnit next = U;
-        if (more) next = quant_next(p, sm, U);
         uint2 raw[Gm::NT][D / 16];          // the next unit's query rows, on their way during the merge
         cw.settle();
         if (round > 0 && !quant_wait<kNapGroup>(sm.combined, (round - 1) & 1, sm.abort)) {
@@ -1087,7 +1127,7 @@ quant_attn_kernel(const QuantParams p) {
             first_seg = split.owner(U.base) + U.u;
             nseg = split.owner(U.base + U.nt - 1) + U.u - first_seg + 1;
         }
-        if (!more || grp == (tend - 1 - t0) % Gm::kGroups) {
+        if (!more || grp == (done - 1) % Gm::kGroups) {
             if (!quant_wait<kNapGroup>(sm.stashed, round & 1, sm.abort)) {
                 *sm.abort = 1;
                 record_error(p.err, kErrWaitGroup);
