@@ -280,6 +280,45 @@ def test_attention_splits(limit, G, Hkv):
     assert torch.equal(a.view(torch.int16), b.view(torch.int16))
 
 
+@pytest.mark.parametrize("B", [31, 32, 33, 100, 1024])
+def test_attention_many_sequences(B):
+    """More sequences than lanes and than CTAs, with empty ones at both ends, in runs and alone."""
+    rng = np.random.RandomState(B)
+    lens = [int(n) if keep else 0 for n, keep in zip(rng.randint(1, 90, B), rng.rand(B) < 0.7)]
+    lens[0] = lens[-1] = 0
+    lens[B // 2] = 700
+    check(make(B, 8, 2, 64, 16, 4, 64, lens, seed=B))
+    lens = [0] * B
+    lens[-1] = 40
+    out = check(make(B, 4, 4, 128, 8, 8, 128, lens, seed=B + 1))
+    assert not bool(out[:-1].any()) and bool(out[-1].any())
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_attention_random(seed):
+    """Drawn shapes: head counts, page sizes, tokens, lengths, grids, bad pages."""
+    rng = np.random.RandomState(1000 + seed)
+    D = int(rng.choice([64, 128]))
+    bits = int(rng.choice([4, 8]))
+    group = int(rng.choice([g for g in (32, 64, 128) if g <= D]))
+    P = int(2 ** rng.randint(3, 9))
+    Hkv = int(rng.choice([1, 2, 3, 4, 5, 6, 8, 12, 16]))
+    sq = int(rng.choice([1, 1, 2, 3, 5]))
+    G = int(rng.choice([g for g in (1, 2, 3, 4, 6, 7, 8, 11, 16, 20, 32, 64) if g * sq <= 64]))
+    B = int(rng.randint(1, 9))
+    top = int(rng.choice([20, 300, 3000]))
+    lens = [int(n) for n in rng.randint(0, top + 1, B)]
+    c = make(B, G * Hkv, Hkv, D, P, bits, group, lens, seed=seed, sq=sq, k_scale=float(rng.choice([1, 4])))
+    if rng.rand() < 0.3:
+        hit = torch.from_numpy(rng.rand(*c["table"].shape) < 0.1).to(DEV)
+        c["table"] = torch.where(hit, torch.full_like(c["table"], 1 << 29), c["table"])
+    B_.decode_attn_set_grid_limit(int(rng.choice([0, 0, 1, 3, 17])))
+    try:
+        check(c, bool(rng.rand() < 0.7), f"D={D} bits={bits} group={group} P={P} Hkv={Hkv} G={G} sq={sq} {lens}")
+    finally:
+        B_.decode_attn_set_grid_limit(0)
+
+
 def test_attention_one_long_sequence():
     """One sequence on every CTA: the merge of many partial rows."""
     check(make(1, 8, 1, 128, 64, 4, 128, [60000], seed=3))
@@ -515,5 +554,9 @@ def test_refused_workspace_and_shapes():
         run(dict(c, q=c["q"].transpose(1, 2)), ws=workspace(c), out=out)
     with pytest.raises(ValueError):
         run(dict(c, lens=c["lens"].cpu()), ws=workspace(c), out=out)
+    with pytest.raises(ValueError):
+        run(dict(c, lens=c["lens"].float()), ws=workspace(c), out=out)
+    with pytest.raises(ValueError):
+        run(dict(c, lens=c["lens"][:1]), ws=workspace(c), out=out)
     with pytest.raises(ValueError):
         run(dict(c, group=128), ws=workspace(c), out=out)

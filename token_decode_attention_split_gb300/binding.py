@@ -339,25 +339,24 @@ def _quant_slots(slot_mapping, T: int, pool):
         _refuse(f"slot_mapping must be a contiguous int64 [{T}] on {pool.device}")
 
 
-def _call_on(index: int, name: str, stream, *args):
-    """Calls a library function (whose last argument is the stream) with CUDA device `index`
-    current: it launches on the current device."""
-    if torch.cuda.current_device() != index:
-        with torch.cuda.device(index):
-            return _call_on(index, name, stream, *args)
-    if stream is None:
-        raw = _current_raw_stream(index)
-    else:
-        raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    status = getattr(_lib or load_library(), name)(*args, raw)
-    if status:
-        _check(status, name)
-
-
-def _current_raw_stream(index: int) -> int:
-    """cudaStream_t of torch's current stream, without building a Stream object where torch can."""
+def _raw_stream(stream, index: int) -> int:
+    """cudaStream_t of `stream`, or of torch's current stream on device `index` (without building a
+    Stream object where torch can)."""
+    if stream is not None:
+        return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
     get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
     return get(index) if get is not None else torch.cuda.current_stream(index).cuda_stream
+
+
+def _call_on(index: int, fn, name: str, *args):
+    """Calls a library function with CUDA device `index` current: it launches on that device."""
+    if torch.cuda.current_device() == index:
+        status = fn(*args)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args)
+    if status:
+        _check(status, name)
 
 
 def decode_attn_append_paged_quant(k_new, v_new, pool, slot_mapping, bits: int, group: int,
@@ -374,9 +373,11 @@ def decode_attn_append_paged_quant(k_new, v_new, pool, slot_mapping, bits: int, 
     _quant_slots(slot_mapping, T, pool)
     if T == 0:
         return
-    _call_on(pool.get_device(), "decode_attn_append_paged_quant", stream, k_new.data_ptr(),
-             v_new.data_ptr(), ks, vs, pool.data_ptr(), slot_mapping.data_ptr(), T, Hkv, D, P,
-             pool.shape[0], bits, group)
+    dev = pool.get_device()
+    _call_on(dev, (_lib or load_library()).decode_attn_append_paged_quant,
+             "decode_attn_append_paged_quant", k_new.data_ptr(), v_new.data_ptr(), ks, vs,
+             pool.data_ptr(), slot_mapping.data_ptr(), T, Hkv, D, P, pool.shape[0], int(bits),
+             int(group), _raw_stream(stream, dev))
 
 
 def decode_attn_read_paged_quant(pool, slot_mapping, k_out, v_out, bits: int, group: int,
@@ -392,9 +393,11 @@ def decode_attn_read_paged_quant(pool, slot_mapping, k_out, v_out, bits: int, gr
     _quant_rows(v_out, "v_out", pool, shape, True)
     _quant_slots(slot_mapping, T, pool)
     if T:
-        _call_on(pool.get_device(), "decode_attn_read_paged_quant", stream, pool.data_ptr(),
-                 slot_mapping.data_ptr(), k_out.data_ptr(), v_out.data_ptr(), T, Hkv, D, P,
-                 pool.shape[0], bits, group)
+        dev = pool.get_device()
+        _call_on(dev, (_lib or load_library()).decode_attn_read_paged_quant,
+                 "decode_attn_read_paged_quant", pool.data_ptr(), slot_mapping.data_ptr(),
+                 k_out.data_ptr(), v_out.data_ptr(), T, Hkv, D, P, pool.shape[0], int(bits),
+                 int(group), _raw_stream(stream, dev))
     return k_out, v_out
 
 
@@ -416,17 +419,18 @@ def decode_attn_paged_quant(q, pool, out, block_table, kv_lens, kv_len_stride: i
             not block_table.is_contiguous() or block_table.get_device() != dev or \
             block_table.shape[0] != B:
         _refuse(f"block_table must be contiguous int32 [{B}, pages] on {pool.device}")
-    if kv_lens.get_device() != dev or not kv_lens.is_contiguous() or kv_lens.element_size() != 4 or \
-            kv_lens.numel() < (B - 1) * kv_len_stride + 1:
-        _refuse(f"kv_lens must hold a contiguous 32-bit length per sequence on {pool.device}")
+    if kv_lens.dtype not in (torch.int32, torch.uint32) or kv_lens.get_device() != dev or \
+            not kv_lens.is_contiguous() or kv_lens.numel() < (B - 1) * kv_len_stride + 1:
+        _refuse(f"kv_lens must hold contiguous 32-bit lengths, one per sequence, on {pool.device}")
     if workspace.get_device() != dev or not workspace.is_contiguous():
         _refuse(f"workspace must be a contiguous buffer on {pool.device}")
     if q.numel():
-        _call_on(dev, "decode_attn_paged_quant", stream, q.data_ptr(), pool.data_ptr(),
-                 out.data_ptr(), block_table.data_ptr(), block_table.shape[1], P, pool.shape[0],
-                 kv_lens.data_ptr(), kv_len_stride, B, Hq, pool.shape[1], D, Sq, bool(causal),
-                 bits, group, softmax_scale, workspace.data_ptr(),
-                 workspace.numel() * workspace.element_size())
+        _call_on(dev, (_lib or load_library()).decode_attn_paged_quant, "decode_attn_paged_quant",
+                 q.data_ptr(), pool.data_ptr(), out.data_ptr(), block_table.data_ptr(),
+                 block_table.shape[1], P, pool.shape[0], kv_lens.data_ptr(), int(kv_len_stride), B,
+                 Hq, pool.shape[1], D, Sq, bool(causal), int(bits), int(group),
+                 float(softmax_scale), workspace.data_ptr(),
+                 workspace.numel() * workspace.element_size(), _raw_stream(stream, dev))
     return out
 
 

@@ -51,6 +51,8 @@
 #include <cuda_runtime.h>
 #include <math_constants.h>
 
+#include <atomic>
+
 #include "f32x2.cuh"
 #include "launch.h"
 #include "ptx.cuh"
@@ -226,14 +228,16 @@ __device__ __forceinline__ QuantUnit quant_next(const QuantParams& p, const Quan
 
 // mbar_wait_warp that naps between its polls, so that a waiting warp leaves the scheduler's issue slots
 // to the others (the twelve consumer warps of the 4-bit kernel are bound by them).
-// Gives up after about a second of naps, or when another thread of the CTA has raised *abort.
+// Gives up after about a second, or when another thread of the CTA has raised *abort.
 template <unsigned NAP_NS>
 __device__ __forceinline__ bool quant_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
     bool done = mbar_try_wait(bar, parity);
     if (!__all_sync(0xffffffffu, done)) {
-        for (unsigned polls = 0; !done && !*abort && polls < kWaitLimitNs / NAP_NS; ++polls) {
+        const uint64_t t0 = global_timer_ns();
+        for (unsigned polls = 1; !done && !*abort; ++polls) {
             __nanosleep(NAP_NS);
             done = mbar_try_wait(bar, parity);
+            if (polls % 64 == 0 && global_timer_ns() - t0 > kWaitLimitNs) break;
         }
         done = __all_sync(0xffffffffu, done);
     }
@@ -1221,9 +1225,19 @@ cudaError_t launch_quant(int groups, bool narrow, const QuantParams& p, int grid
 template <int D, int BITS, int NG, int NC>
 cudaError_t launch_quant_as(const QuantParams& p, int grid, cudaStream_t st) {
     using Gm = QuantGeometry<D, BITS, NG, NC>;
+    const void* kernel = reinterpret_cast<const void*>(&quant_attn_kernel<D, BITS, NG, NC>);
+    // The consumers' share of registers must be there: a build that gives the launch fewer (other compiler
+    // flags) would leave them waiting for it.
+    static std::atomic<int> launch_regs{0};
+    if (launch_regs.load() == 0) {
+        cudaFuncAttributes a;
+        const cudaError_t e = cudaFuncGetAttributes(&a, kernel);
+        if (e != cudaSuccess) return e;
+        launch_regs.store(a.numRegs);
+    }
+    if (launch_regs.load() != Gm::kLaunchRegs) return cudaErrorInvalidConfiguration;
     void* args[] = {const_cast<QuantParams*>(&p)};
-    return launch_configured(reinterpret_cast<const void*>(&quant_attn_kernel<D, BITS, NG, NC>),
-                             Gm::kSmemBytes, grid, Gm::kThreads, st, args);
+    return launch_configured(kernel, Gm::kSmemBytes, grid, Gm::kThreads, st, args);
 }
 
 template <int D, int BITS>
