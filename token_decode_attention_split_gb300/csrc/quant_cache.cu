@@ -67,6 +67,15 @@ struct CacheArgs {
 constexpr float kRound = 12582912.0f;
 constexpr uint32_t kRoundBits = 0x4b400000u;
 
+// The largest float at or below 1 / s, for a normal s below 2^126: an approximate reciprocal, one
+// Newton step, and a step of one unit down where the (exactly signed) residual says it is above.
+__device__ __forceinline__ float below_reciprocal(float s) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+    r = __fmaf_rn(r, __fmaf_rn(-s, r, 1.0f), r);
+    return __fmaf_rn(-s, r, 1.0f) < 0.f ? __uint_as_float(__float_as_uint(r) - 1u) : r;
+}
+
 template <int D, int BITS>
 struct RowShape {
     static constexpr int kWords = D * BITS / 32;          // words of a stored row = lanes per row
@@ -155,7 +164,7 @@ __device__ __forceinline__ uint32_t quantise_word(
         if (!fine || s < 1.17549435e-38f) s = 0.f;
         par[q] = fine ? (__float_as_uint(s) >> 16) | (__float_as_uint(mn) & 0xffff0000u)
                       : 0x7fc07fc0u;
-        const float inv = s > 0.f ? __frcp_rz(s) : 0.f;
+        const float inv = s > 0.f ? below_reciprocal(s) : 0.f;
         const float base = fine ? mn : 0.f;
         const f2 inv2 = f2_of(inv, inv), down = f2_of(-base, -base), minus = f2_of(-s, -s);
         const f2 up = f2_of(kRound, kRound), back = f2_of(-kRound, -kRound);
@@ -202,11 +211,12 @@ __device__ __forceinline__ unsigned char* slot_block(const CacheArgs& a, int64_t
 
 // Work of both kernels: a unit is `span` KV heads of one row, a warp takes one unit after another;
 // 32 / kWords heads go through the warp at a time, so many times, with the loads of all steps in flight
-// together.  The writer computes about 75 instructions per (row, KV head) and is fastest with two steps
-// and twice the CTAs that fit, so that new ones load while old ones compute (8192 rows of 8 heads, with
-// the rows read back: 22.0 us; four steps 24.5, one step 24.4, a grid of resident CTAs 25.1).  The reader
-// is bound by memory: four steps on a resident grid (131071 rows of 8 heads: 109.6 us, 6.28 TB/s; two
-// steps 116.5, twice the CTAs 115.2).
+// together.  The writer issues about 150 instructions per (row, KV head), a third of them for the groups'
+// minima, maxima and scales, and is bound by issue and the latency of its first loads; it is fastest with
+// two steps and twice the CTAs that fit, so that new ones load while old ones compute (8192 rows of 8
+// heads in groups of 32, with the rows read back: 21.9 us; four steps 24.5, one step 24.4, a grid of
+// resident CTAs 25.1).  The reader is bound by memory: four steps on a resident grid (131071 rows of 8
+// heads: 109.6 us, 6.28 TB/s; two steps 116.5, twice the CTAs 115.2).
 constexpr int kCtasPerSm = 4;
 constexpr int kReadSteps = 4, kAppendSteps = 2;
 constexpr int kReadWaves = 1, kAppendWaves = 2;
