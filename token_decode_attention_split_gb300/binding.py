@@ -15,6 +15,7 @@ import torch
 from . import build as _build
 
 DA_VARIANT_DENSE, DA_VARIANT_PAGED, DA_VARIANT_SPARSE, DA_VARIANT_PAGED_QUANT = 0, 1, 2, 3
+_U8, _I32, _I64, _BF16 = torch.uint8, torch.int32, torch.int64, torch.bfloat16
 _lock = threading.Lock()
 _lib = None
 
@@ -308,23 +309,23 @@ def _refuse(what: str):
     raise ValueError(what)
 
 
-def _quant_page_size(pool, D: int, bits: int, group: int) -> int:
-    """Page size of a quantised pool [num_pages, Hkv, page_bytes]."""
-    if pool.dtype != torch.uint8 or pool.dim() != 3 or not pool.is_contiguous() or not pool.is_cuda:
+def _quant_page_size(pool, dev: int, D: int, bits: int, group: int) -> int:
+    """Page size of a quantised pool [num_pages, Hkv, page_bytes] on CUDA device `dev`."""
+    if dev < 0 or pool.dtype is not _U8 or pool.dim() != 3 or not pool.is_contiguous():
         _refuse("pool must be a contiguous uint8 CUDA tensor [num_pages, Hkv, page_bytes]")
     if D <= 0 or bits <= 0 or group <= 0 or D % group:
         _refuse(f"no rows of {D} elements in groups of {group} with {bits} bits")
     row = 2 * D * bits // 8 + D // group * 8
-    nbytes = pool.shape[2]
+    nbytes = pool.size(2)
     if nbytes == 0 or nbytes % row:
         _refuse(f"pages of {nbytes} bytes hold no whole rows of {row} bytes")
     return nbytes // row
 
 
-def _quant_rows(t, name: str, pool, shape, contiguous: bool) -> int:
+def _quant_rows(t, name: str, dev: int, shape, contiguous: bool) -> int:
     """Checks bf16 rows [T, Hkv, D] beside a pool; their row stride in elements."""
-    if t.dtype != torch.bfloat16 or t.shape != shape or t.get_device() != pool.get_device():
-        _refuse(f"{name} must be bf16 {list(shape)} on {pool.device}")
+    if t.dtype is not _BF16 or t.get_device() != dev or t.shape != shape:
+        _refuse(f"{name} must be bf16 {list(shape)} on cuda:{dev}")
     if t.is_contiguous():
         return shape[1] * shape[2]
     if contiguous or t.stride(2) != 1 or (shape[1] > 1 and t.stride(1) != shape[2]):
@@ -333,10 +334,10 @@ def _quant_rows(t, name: str, pool, shape, contiguous: bool) -> int:
     return t.stride(0) if shape[0] > 1 else shape[1] * shape[2]
 
 
-def _quant_slots(slot_mapping, T: int, pool):
-    if slot_mapping.dtype != torch.int64 or slot_mapping.shape != (T,) or \
-            not slot_mapping.is_contiguous() or slot_mapping.get_device() != pool.get_device():
-        _refuse(f"slot_mapping must be a contiguous int64 [{T}] on {pool.device}")
+def _quant_slots(slot_mapping, T: int, dev: int):
+    if slot_mapping.dtype is not _I64 or slot_mapping.get_device() != dev or \
+            slot_mapping.dim() != 1 or slot_mapping.size(0) != T or not slot_mapping.is_contiguous():
+        _refuse(f"slot_mapping must be a contiguous int64 [{T}] on cuda:{dev}")
 
 
 def _raw_stream(stream, index: int) -> int:
@@ -365,18 +366,18 @@ def decode_attn_append_paged_quant(k_new, v_new, pool, slot_mapping, bits: int, 
     (int64 [T]) of a quantised pool [num_pages,Hkv,page_bytes] (new_quant_pool)."""
     shape = k_new.shape
     T, Hkv, D = shape
-    P = _quant_page_size(pool, D, bits, group)
-    if pool.shape[1] != Hkv:
-        _refuse(f"rows of {Hkv} KV heads beside a pool of {pool.shape[1]}")
-    ks = _quant_rows(k_new, "k_new", pool, shape, False)
-    vs = _quant_rows(v_new, "v_new", pool, shape, False)
-    _quant_slots(slot_mapping, T, pool)
+    dev = pool.get_device()
+    P = _quant_page_size(pool, dev, D, bits, group)
+    if pool.size(1) != Hkv:
+        _refuse(f"rows of {Hkv} KV heads beside a pool of {pool.size(1)}")
+    ks = _quant_rows(k_new, "k_new", dev, shape, False)
+    vs = _quant_rows(v_new, "v_new", dev, shape, False)
+    _quant_slots(slot_mapping, T, dev)
     if T == 0:
         return
-    dev = pool.get_device()
     _call_on(dev, (_lib or load_library()).decode_attn_append_paged_quant,
              "decode_attn_append_paged_quant", k_new.data_ptr(), v_new.data_ptr(), ks, vs,
-             pool.data_ptr(), slot_mapping.data_ptr(), T, Hkv, D, P, pool.shape[0], int(bits),
+             pool.data_ptr(), slot_mapping.data_ptr(), T, Hkv, D, P, pool.size(0), int(bits),
              int(group), _raw_stream(stream, dev))
 
 
@@ -386,17 +387,17 @@ def decode_attn_read_paged_quant(pool, slot_mapping, k_out, v_out, bits: int, gr
     [T,Hkv,D], contiguous); a slot outside the pool gives zero rows."""
     shape = k_out.shape
     T, Hkv, D = shape
-    P = _quant_page_size(pool, D, bits, group)
-    if pool.shape[1] != Hkv:
-        _refuse(f"rows of {Hkv} KV heads beside a pool of {pool.shape[1]}")
-    _quant_rows(k_out, "k_out", pool, shape, True)
-    _quant_rows(v_out, "v_out", pool, shape, True)
-    _quant_slots(slot_mapping, T, pool)
+    dev = pool.get_device()
+    P = _quant_page_size(pool, dev, D, bits, group)
+    if pool.size(1) != Hkv:
+        _refuse(f"rows of {Hkv} KV heads beside a pool of {pool.size(1)}")
+    _quant_rows(k_out, "k_out", dev, shape, True)
+    _quant_rows(v_out, "v_out", dev, shape, True)
+    _quant_slots(slot_mapping, T, dev)
     if T:
-        dev = pool.get_device()
         _call_on(dev, (_lib or load_library()).decode_attn_read_paged_quant,
                  "decode_attn_read_paged_quant", pool.data_ptr(), slot_mapping.data_ptr(),
-                 k_out.data_ptr(), v_out.data_ptr(), T, Hkv, D, P, pool.shape[0], int(bits),
+                 k_out.data_ptr(), v_out.data_ptr(), T, Hkv, D, P, pool.size(0), int(bits),
                  int(group), _raw_stream(stream, dev))
     return k_out, v_out
 
@@ -408,27 +409,27 @@ def decode_attn_paged_quant(q, pool, out, block_table, kv_lens, kv_len_stride: i
     DA_VARIANT_PAGED_QUANT, B, Hq * Sq, Hkv, D)."""
     shape = q.shape
     B, Hq, Sq, D = shape
-    P = _quant_page_size(pool, D, bits, group)
     dev = pool.get_device()
-    if q.dtype != torch.bfloat16 or not q.is_contiguous() or q.get_device() != dev:
-        _refuse(f"q must be contiguous bf16 on {pool.device}")
-    if out.dtype != torch.bfloat16 or not out.is_contiguous() or out.get_device() != dev or \
-            out.shape != shape:
-        _refuse(f"out must be contiguous bf16 of q's shape on {pool.device}")
-    if block_table.dtype != torch.int32 or block_table.dim() != 2 or \
-            not block_table.is_contiguous() or block_table.get_device() != dev or \
-            block_table.shape[0] != B:
-        _refuse(f"block_table must be contiguous int32 [{B}, pages] on {pool.device}")
-    if kv_lens.dtype not in (torch.int32, torch.uint32) or kv_lens.get_device() != dev or \
-            not kv_lens.is_contiguous() or kv_lens.numel() < (B - 1) * kv_len_stride + 1:
-        _refuse(f"kv_lens must hold contiguous 32-bit lengths, one per sequence, on {pool.device}")
+    P = _quant_page_size(pool, dev, D, bits, group)
+    if q.dtype is not _BF16 or q.get_device() != dev or not q.is_contiguous():
+        _refuse(f"q must be contiguous bf16 on cuda:{dev}")
+    if out.dtype is not _BF16 or out.get_device() != dev or out.shape != shape or \
+            not out.is_contiguous():
+        _refuse(f"out must be contiguous bf16 of q's shape on cuda:{dev}")
+    if block_table.dtype is not _I32 or block_table.get_device() != dev or block_table.dim() != 2 or \
+            block_table.size(0) != B or not block_table.is_contiguous():
+        _refuse(f"block_table must be contiguous int32 [{B}, pages] on cuda:{dev}")
+    if (kv_lens.dtype is not _I32 and kv_lens.dtype is not torch.uint32) or \
+            kv_lens.get_device() != dev or kv_lens.numel() < (B - 1) * kv_len_stride + 1 or \
+            not kv_lens.is_contiguous():
+        _refuse(f"kv_lens must hold contiguous 32-bit lengths, one per sequence, on cuda:{dev}")
     if workspace.get_device() != dev or not workspace.is_contiguous():
-        _refuse(f"workspace must be a contiguous buffer on {pool.device}")
+        _refuse(f"workspace must be a contiguous buffer on cuda:{dev}")
     if q.numel():
         _call_on(dev, (_lib or load_library()).decode_attn_paged_quant, "decode_attn_paged_quant",
                  q.data_ptr(), pool.data_ptr(), out.data_ptr(), block_table.data_ptr(),
-                 block_table.shape[1], P, pool.shape[0], kv_lens.data_ptr(), int(kv_len_stride), B,
-                 Hq, pool.shape[1], D, Sq, bool(causal), int(bits), int(group),
+                 block_table.size(1), P, pool.size(0), kv_lens.data_ptr(), int(kv_len_stride), B,
+                 Hq, pool.size(1), D, Sq, bool(causal), int(bits), int(group),
                  float(softmax_scale), workspace.data_ptr(),
                  workspace.numel() * workspace.element_size(), _raw_stream(stream, dev))
     return out
