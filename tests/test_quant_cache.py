@@ -503,6 +503,64 @@ def test_serving_loop(bits, group):
     assert B_.decode_attn_read_device_error() == 0
 
 
+def test_two_graphs_share_a_workspace():
+    """Two captured calls of unlike shapes on one workspace, replayed in turn."""
+    a = make(4, 32, 8, 128, 16, 4, 128, [3000, 17, 0, 900], seed=101)
+    b = make(9, 16, 1, 64, 32, 8, 32, [500, 1, 40, 2000, 0, 7, 64, 333, 90], seed=102)
+    ws = max(workspace(a), workspace(b), key=lambda w: w.numel())
+    want = [run(c).view(torch.int16).clone() for c in (a, b)]
+    outs, graphs = [], []
+    for c in (a, b):
+        out = torch.empty_like(c["q"])
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            run(c, ws=ws, out=out)
+        outs.append(out)
+        graphs.append(g)
+    for i in (0, 1, 1, 0, 0, 1):
+        outs[i].fill_(float("nan"))
+        graphs[i].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[i].view(torch.int16), want[i])
+
+
+FIRST_CALL = """
+import torch
+from token_decode_attention_split_gb300 import binding as B
+k = torch.randn(40, 2, 64, device="cuda").to(torch.bfloat16)
+pool = B.new_quant_pool(4, 2, 64, 16, 4, 64, "cuda")
+slots = torch.arange(40, device="cuda")
+table = torch.arange(4, dtype=torch.int32, device="cuda")[None]
+lens = torch.tensor([40], dtype=torch.int32, device="cuda")
+q = torch.randn(1, 8, 1, 64, device="cuda").to(torch.bfloat16)
+out, back = torch.zeros_like(q), torch.empty_like(k)
+ws = B.new_workspace(B.decode_attn_workspace_size(B.DA_VARIANT_PAGED_QUANT, 1, 8, 2, 64), "cuda")
+def calls():
+    B.decode_attn_append_paged_quant(k, k, pool, slots, 4, 64)
+    B.decode_attn_read_paged_quant(pool, slots, back, torch.empty_like(k), 4, 64)
+    B.decode_attn_paged_quant(q, pool, out, table, lens, 1, 4, 64, False, 0.125, ws)
+g = torch.cuda.CUDAGraph()
+torch.cuda.synchronize()
+with torch.cuda.graph(g):
+    calls()
+g.replay()
+torch.cuda.synchronize()
+captured = out.clone()
+calls()
+torch.cuda.synchronize()
+assert torch.equal(captured, out) and bool(out.any())
+"""
+
+
+def test_first_call_inside_a_capture():
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
 def test_two_streams_at_once():
     """Two calls in flight together on one pool, each with a workspace of its own."""
     c = make(4, 32, 8, 128, 16, 4, 128, [3000, 17, 2000, 900], seed=95)
