@@ -319,10 +319,104 @@ def test_attention_random(seed):
         B_.decode_attn_set_grid_limit(0)
 
 
+@pytest.mark.parametrize("D,bits", [(64, 4), (64, 8), (128, 4), (128, 8)])
+@pytest.mark.parametrize("G,sq", [(33, 1), (64, 1), (8, 5), (1, 64)])
+@pytest.mark.parametrize("P", [8, 64, 256])
+def test_attention_wide_units(D, bits, G, sq, P):
+    """33 to 64 columns of rows with one group: lengths around a stage, several KV heads, lost pages, causal or
+    not, units in one piece and in many."""
+    lens = [0, 1, 63, 64, 65, 700, 128, sq, 0]
+    c = make(len(lens), 3 * G, 3, D, P, bits, D, lens, seed=D + bits + G + P, sq=sq)
+    ws = workspace(c)
+    for limit in (0, 1, 5):
+        B_.decode_attn_set_grid_limit(limit)
+        try:
+            for causal in (True, False):
+                R.check(run(c, causal, ws), *oracle(c, causal), f"limit {limit} causal {causal}")
+        finally:
+            B_.decode_attn_set_grid_limit(0)
+    c["table"][5, ::2] = 1 << 30
+    c["table"][2] = -5
+    check(c)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("k_scale,v_scale,q_scale", [(30.0, 1.0, 1.0), (1.0, 1e-6, 1.0), (1.0, 1e20, 1.0),
+                                                     (1e-3, 1.0, 1e4), (1.0, 1.0, 1e-30), (1e-25, 1.0, 1e25)])
+def test_attention_wide_magnitudes(bits, k_scale, v_scale, q_scale):
+    c = make(2, 80, 2, 128, 16, bits, 128, [500, 33], seed=42, k_scale=k_scale, v_scale=v_scale)
+    c["q"] = (c["q"].float() * q_scale).to(BF)
+    check(c)
+    for scale in (0.0, -0.125):
+        check(dict(c, scale=scale * c["scale"]))
+
+
+def test_attention_wide_rows_of_unlike_scale():
+    """Scores and V scales that grow along the sequence, together and against each other: the references
+    rise many times, in either half of a tile."""
+    D, P, n = 128, 16, 640
+    c = make(1, 40, 1, D, P, 4, D, [n], seed=53)
+    g = gen(54)
+    q = normals(g, 1, 40, 1, D)
+    q[:] = q[:, :1]
+    pos = torch.arange(n, device=DEV)
+    grow = torch.linspace(-1.0, 1.0, n, device=DEV)[:, None, None]
+    slots = c["table"][0, pos // P].long() * P + pos % P
+    for sign, order in ((1.0, 1.0), (1.0, -1.0), (-1.0, 1.0)):
+        k = (sign * grow * q[0, 0].float() * 4.0 + 0.1 * torch.randn(n, 1, D, generator=g, device=DEV)).to(BF)
+        v = (torch.randn(n, 1, D, generator=g, device=DEV) * torch.exp2(order * 30.0 * grow)).to(BF)
+        v[5::7] = 0
+        B_.decode_attn_append_paged_quant(k, v, c["pool"], slots, 4, D)
+        c["q"] = q
+        out = run(c)
+        ref, _ = oracle(c)
+        kk, vv = R.rows(c["pool"].cpu().numpy(), (slots // P).cpu().numpy(), (slots % P).cpu().numpy(), D, P, 4, D)
+        x = c["scale"] * (R.f64(q)[0, 0, 0] @ kk[0][:, 0].T)
+        p = np.exp(x - x.max())
+        w = (p / p.sum())[:, None]
+        # as above: weights to fp16 (subnormals: half of 2^-24 of the largest weight * scale), scores to fp32
+        d = 2.0 ** -18 * c["scale"] * np.abs(R.f64(q)[0, 0, 0]).sum() * (np.abs(kk[2]) + 15 * kk[1]).max()
+        tol = 2.0 ** -8 * np.abs(ref[0, 0, 0]) + (w * (
+            (2.0 ** -11 + 2.0 ** -15 + 2 * d) * (15 * vv[1][:, 0] + np.abs(vv[2][:, 0])))).sum(0)
+        tol = tol + 2.0 ** -25 * 15 * n * (w * vv[1][:, 0]).max(0)
+        for i in range(40):
+            R.check(out[0, i, 0], ref[0, i, 0], tol, f"sign {sign} order {order}")
+
+
+def test_attention_wide_nan_rows():
+    """A NaN in the last row reaches the last token's columns only, of its sequence."""
+    D, P = 64, 16
+    c = make(3, 40, 2, D, P, 8, D, [100, 100, 100], seed=63, sq=2)
+    g = gen(64)
+    for b, which in ((0, 0), (1, 1)):
+        kv = [normals(g, 1, 2, D), normals(g, 1, 2, D)]
+        kv[which][0, 1, 40] = float("nan")
+        slot = c["table"][b, 99 // P].long() * P + 99 % P
+        B_.decode_attn_append_paged_quant(kv[0], kv[1], c["pool"], slot.reshape(1), 8, D)
+    out = check(c, True).float()
+    assert bool(torch.isnan(out[:2, 20:, 1]).all())
+    assert not bool(torch.isnan(out[:, :20]).any()) and not bool(torch.isnan(out[:, :, 0]).any())
+    assert not bool(torch.isnan(out[2]).any())
+
+
+def test_attention_wide_mixed_with_narrow():
+    """Calls of both kernels one behind the other on one stream and one workspace."""
+    a = make(3, 64, 1, 128, 16, 4, 128, [2000, 31, 450], seed=81)
+    b = make(5, 32, 8, 128, 16, 4, 128, [900, 0, 64, 2500, 1], seed=82)
+    ws = max(workspace(a), workspace(b), key=lambda t: t.numel())
+    want = [run(c).view(torch.int16).clone() for c in (a, b)]
+    outs = []
+    for i in range(20):
+        outs.append(run((a, b)[i % 2], ws=ws))
+    for i, out in enumerate(outs):
+        assert torch.equal(out.view(torch.int16), want[i % 2])
+
+
 def test_attention_one_long_sequence():
     """One sequence on every CTA: the merge of many partial rows."""
     check(make(1, 8, 1, 128, 64, 4, 128, [60000], seed=3))
     check(make(2, 8, 2, 64, 256, 8, 32, [30001, 12345], seed=4))
+    check(make(1, 64, 1, 128, 16, 4, 128, [40001], seed=5))
 
 
 def test_attention_stride_3_and_clamped_lengths():

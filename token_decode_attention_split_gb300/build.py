@@ -16,7 +16,7 @@ LIB = os.path.join(BUILD, "libdecode_attn.so")
 SOURCES = ["api.cu", "kernels_dense.cu", "kernels_paged.cu", "kernels_paged_multi.cu",
            "kernels_sparse.cu", "sparse_tc.cu", "noalloc.cu", "append.cu", "wait_check.cu",
            "quant_cache.cu", "kernels_quant4_d64.cu", "kernels_quant4_d128.cu",
-           "kernels_quant8_d64.cu", "kernels_quant8_d128.cu"]
+           "kernels_quant8_d64.cu", "kernels_quant8_d128.cu", "quant_tc.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

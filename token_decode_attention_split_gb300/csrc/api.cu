@@ -213,6 +213,15 @@ int quant_kv_heads(int B, int Hkv, int cols, int bits, int sms) {
 // places 176.5.
 int quant_unit_pad(int cols) { return cols <= 8 ? 5 : cols <= 16 ? 4 : 2; }
 
+// The tcgen05 kernel takes more than 32 columns of rows with one group: its time does not depend on the
+// columns, the other's grows with every 16 (a 16-row tile in L2, 4 bits: 196 ns for any number of columns
+// against 93, 158 and 292 for 16, 32 and 64; 8 bits, 64 columns: 252 against 376).  At 64 columns 32 ragged
+// sequences take 39.7 us against 50.1, 32 of 16000 rows 55 against 75, 32 of 300 rows 14.7 against 15.5, one
+// of 4000 rows 20.8 against 19.1; at 32 columns 32 of 8000 rows 31.6 against 28.4.  Its stages are of 64 rows:
+// 8 empty places (the ragged sequences with 4: 46.0 us, with 16: 41.9).
+bool quant_uses_tc(int cols, int groups) { return groups == 1 && cols > 32; }
+constexpr int kQuantTcUnitPad = 8;
+
 // CTAs for a persistent dense/paged launch on `dev`.
 int persistent_ctas(int dev) {
     const int sms = sm_count(dev);
@@ -680,7 +689,8 @@ extern "C" da_status decode_attn_paged_quant(
     if (sms <= 0) return DA_ERR_CUDA;
     QuantParams p{};
     p.cols = (Hq / Hkv) * Sq;
-    const int kh = quant_kv_heads(B, Hkv, p.cols, bits, sms);
+    const bool tc = quant_uses_tc(p.cols, D / group);
+    const int kh = tc ? 1 : quant_kv_heads(B, Hkv, p.cols, bits, sms);
     while ((1 << p.kh_shift) < kh) ++p.kh_shift;
     p.upb = Hkv / kh;
     const long long qunits = units / kh;
@@ -701,7 +711,7 @@ extern "C" da_status decode_attn_paged_quant(
     p.sq = Sq;
     p.causal = causal ? 1 : 0;
     p.slices_shift = quant_slices_shift(p.cols);
-    p.unit_pad = quant_unit_pad(p.cols);
+    p.unit_pad = tc ? kQuantTcUnitPad : quant_unit_pad(p.cols);
     p.scale_log2 = softmax_scale * 1.4426950408889634f;
     unsigned char* base = static_cast<unsigned char*>(workspace);
     p.counters = reinterpret_cast<unsigned*>(base + w.counters);
@@ -712,9 +722,10 @@ extern "C" da_status decode_attn_paged_quant(
     const bool narrow = p.cols <= 8;
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
     const cudaError_t e =
-        D == 64 ? (bits == 4 ? launch_quant<64, 4>(groups, narrow, p, grid, cs)
-                             : launch_quant<64, 8>(groups, narrow, p, grid, cs))
-                : (bits == 4 ? launch_quant<128, 4>(groups, narrow, p, grid, cs)
-                             : launch_quant<128, 8>(groups, narrow, p, grid, cs));
+        tc        ? launch_quant_tc(D, bits, p, grid, cs)
+        : D == 64 ? (bits == 4 ? launch_quant<64, 4>(groups, narrow, p, grid, cs)
+                               : launch_quant<64, 8>(groups, narrow, p, grid, cs))
+                  : (bits == 4 ? launch_quant<128, 4>(groups, narrow, p, grid, cs)
+                               : launch_quant<128, 8>(groups, narrow, p, grid, cs));
     return e == cudaSuccess ? DA_OK : DA_ERR_CUDA;
 }

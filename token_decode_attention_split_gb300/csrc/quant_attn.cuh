@@ -32,14 +32,14 @@
 // on N, each with a running state of its own, merged once per segment.
 //
 // What bounds it.  8-bit codes: HBM.  4-bit codes halve the bytes and leave 48 ns of HBM time per
-// 16-row tile and SM (D = 128, 136 bytes a row) for about 200 warp instructions, 104 of them the masks,
+// 16-row tile and SM (D = 128, 136 bytes a row) for about 225 warp instructions, 104 of them the masks,
 // shifts and byte permutes that make fp16 operands (two cycles each on their pipe): the kernel is issue
-// bound at about 56 ns a tile (measured with the cache in L2), so everything around the tiles is kept
+// bound at about 53 ns a tile (measured with the cache in L2), so everything around the tiles is kept
 // off the schedulers.  Twelve consumer warps of 160 registers in three groups, each on every third
 // stage, and three copying warps: 64 ns a tile (66 with eight consumer warps in one group, 71 with
 // sixteen of 112 registers; 74 with one copying warp, whose lookup, wait and copy take longer than a
 // stage); fp32 arithmetic on register pairs (f32x2) and waits that nap instead of polling: 62 ns; warp
-// indices broadcast, so that no warp-wide instruction needs a convergence check: 56 ns.
+// indices broadcast, so that no warp-wide instruction needs a convergence check: 56 ns; cheaper ends: 53 ns.
 //
 // A segment that covers its unit writes the output; any other writes its normalised partial rows
 // and log2-sum-exps, and the CTA that completes the unit (an acquire-release counter) merges them
@@ -120,7 +120,8 @@ struct QuantGeometry {
     static constexpr int kStages =
         (kStagesFit > kMaxStages ? kMaxStages : kStagesFit) / kCopyWarps * kCopyWarps;
     static constexpr int kSmemBytes = 128 + kStages * kStageBytes + kFixedBytes;
-    static_assert(kCopyWarps <= 3 && kStages >= kCopyWarps && kStages >= 2 && kStages % kCopyWarps == 0 && kStages % kGroups == 0 && kStageBytes % 128 == 0 && kTiles >= WG, "ring");
+    static_assert(kCopyWarps <= 3 && kStages >= 2 && kStages >= kCopyWarps && kStages % kCopyWarps == 0 &&
+                  kStages % kGroups == 0 && kStageBytes % 128 == 0 && kTiles >= WG, "ring");
 };
 
 struct QuantSmem {
@@ -761,11 +762,12 @@ __device__ __forceinline__ void store_row4(__nv_bfloat16* p, float4 v) {
 
 // Merges the nseg partial rows of a unit by log-sum-exp in segment order and stores its output.  A
 // thread keeps the loads of kAhead segments of kRows rows in flight: a unit costs one trip to L2 per kAhead
-// segments and kRows * kConsumers / (D / 4) rows (the narrow kernels' units have few rows).
+// segments and kRows * kConsumers / (D / 4) rows (twice the segments of half the rows: 51.4 instead of 50.2 us
+// for 64 columns of 32 ragged sequences; twice as many in flight costs the streaming loop registers: 53).
 template <class Gm>
 __device__ __forceinline__ void quant_merge_unit(const QuantParams& p, size_t row0, int first_seg,
                                                  int nseg) {
-    constexpr int D4 = Gm::D / 4, kAhead = 8, kRows = Gm::NT, kHop = Gm::kConsumers / D4;
+    constexpr int D4 = Gm::D / 4, kAhead = 4, kRows = 2 * Gm::NT, kHop = Gm::kConsumers / D4;
     const int SH = p.cols << p.kh_shift, d4 = threadIdx.x % D4;
     const float* lse = p.part_lse + static_cast<size_t>(first_seg) * SH;
     const float4* o = reinterpret_cast<const float4*>(p.part_o + static_cast<size_t>(first_seg) * SH * Gm::D) + d4;
@@ -1221,6 +1223,9 @@ quant_attn_kernel(const QuantParams p) {
 // most 8 query columns per KV head.
 template <int D, int BITS>
 cudaError_t launch_quant(int groups, bool narrow, const QuantParams& p, int grid, cudaStream_t st);
+
+// The tcgen05 kernel (quant_tc.cu): one group per row, 33 to 64 query columns per KV head.
+cudaError_t launch_quant_tc(int D, int bits, const QuantParams& p, int grid, cudaStream_t st);
 
 template <int D, int BITS, int NG, int NC>
 cudaError_t launch_quant_as(const QuantParams& p, int grid, cudaStream_t st) {

@@ -426,7 +426,7 @@ da_status launch(Kernel kernel, bool read, CacheArgs& a, void* pool, const int64
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-        const int64_t most = static_cast<int64_t>(kCtasPerSm) * (read ? kReadWaves : kAppendWaves) * sms;
+    const int64_t most = static_cast<int64_t>(kCtasPerSm) * (read ? kReadWaves : kAppendWaves) * sms;
     cfg.gridDim = dim3(static_cast<unsigned>(want < most ? want : most));
     cfg.blockDim = dim3(kThreads);
     cfg.stream = static_cast<cudaStream_t>(stream);
