@@ -14,7 +14,7 @@
 // The weights p_j vs_j are rounded to fp16 (2^-11 relative) for the product with the V codes.  They
 // are kept near 1 by a reference of their own: m is the reference of the softmax, M that of
 // x_j + log2 vs_j, and f = 2^(m - M).  Both are raised only when a weight passes 2^8, so the usual
-// tile has no cross-lane maximum at all; sums stay in fp32 and are exact in the reference.
+// tile has no cross-lane maximum at all.  The result is the same for any reference; sums stay in fp32.
 //
 // V's codes are taken about their middle code: sum w c = sum w (c - mid) + mid sum w, the second sum
 // in fp32 (it joins vmin) and the first as the product minus mid times the sum of the rounded weights
