@@ -132,7 +132,7 @@ struct QuantSmem {
     uint64_t* full;
     uint64_t* empty;
     uint64_t* group;         // all consumers
-    uint64_t* stashed;       // the merge slots hold every warp's columns of this round
+    uint64_t* stashed;       // the merge slots hold every warp's columns of a segment
     uint64_t* combined;      // they have been merged and may be written again
     int* stage_len;          // rows per head of the stage inside the sequence; -1: every row counts
     unsigned* stage_pages;   // bit i: page i of the stage was copied

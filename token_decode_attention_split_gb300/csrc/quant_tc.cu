@@ -64,7 +64,7 @@ struct TcQuant {
     static constexpr int kRowStride = D / 2 + 4;             // floats between the rows handed over
     static constexpr int kOffHalf = kOffParam + kBuffers * kParamBytes;
     static constexpr int kOffRing = kOffHalf + 2 * kMaxCols * kRowStride * 4;
-    static constexpr int kMiscBytes = 3072;
+    static constexpr int kMiscBytes = 3 * 1024;
     static constexpr int kSchedBytes = (2 * kMaxPagedBatch + 2) * 4;
     static constexpr int kFit = (kSmemBudget - 1024 - kOffRing - kMiscBytes - kSchedBytes) / kStageBytes;
     static constexpr int kStages = kFit > kMaxStages ? kMaxStages : kFit;
@@ -112,7 +112,7 @@ struct TcQuantBars {
     float q_cf[2][kMaxCols], q_sum[2][kMaxCols];
     float half_m[2][kMaxCols], half_l[2][kMaxCols];
 };
-static_assert(sizeof(TcQuantBars) <= 3072, "barrier block");
+static_assert(sizeof(TcQuantBars) <= 3 * 1024, "barrier block");
 
 // kind::f16 with fp16 operands, A K-major (tensor memory), B K-major or MN-major
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn_major) {
